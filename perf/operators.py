@@ -214,7 +214,7 @@ def prepare(case, seed):
     else:
         # a policy that has moved towards the chosen answers
         which = torch.searchsorted(cuts[1:].contiguous(), torch.arange(n, device="cuda"), right=True)
-        s["ref_logp"] = now - 0.3 * (1.0 - 2.0 * (which % 2)) + noise(0.2)
+        s["ref_logp"] = now - min(0.3, 15.0 / mean) * (1.0 - 2.0 * (which % 2)) + noise(0.2)
         s["dlogp"] = torch.empty(n, **f)
         s["pair_loss"], s["margins"] = torch.empty(case["pairs"], **f), torch.empty(case["pairs"], **f)
     return s
