@@ -1,0 +1,193 @@
+// z1_ops_internal.h -- what the host code of the operators (z1_ops_api.hip)
+// and their kernels (z1_muon.hip, z1_embed.hip, z1_loss.hip) share.  Not
+// installed.
+#pragma once
+
+#include <hip/hip_fp16.h>
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "z1_ops.h"
+
+namespace z1 {
+namespace ops {
+
+typedef _Float16 half4 __attribute__((ext_vector_type(4)));
+typedef _Float16 half8 __attribute__((ext_vector_type(8)));
+typedef float float4v __attribute__((ext_vector_type(4)));
+typedef float float16v __attribute__((ext_vector_type(16)));
+typedef uint32_t uint4v __attribute__((ext_vector_type(4)));
+typedef uint32_t uint2v __attribute__((ext_vector_type(2)));
+
+constexpr int kWaveLanes = 64;
+
+// bf16 <-> fp32, to nearest even, NaN kept (quiet).
+__device__ __forceinline__ float bf16_to_f32(uint16_t h)
+{
+    return __uint_as_float((uint32_t)h << 16);
+}
+__device__ __forceinline__ uint16_t f32_to_bf16(float x)
+{
+    const uint32_t u = __float_as_uint(x);
+    if ((u & 0x7fffffffu) > 0x7f800000u)
+        return (uint16_t)((u >> 16) | 0x40u);
+    return (uint16_t)((u + 0x7fffu + ((u >> 16) & 1u)) >> 16);
+}
+
+// Element types of the operators' tensors: storage, and conversion from and
+// to fp32 (to nearest even).
+struct F32 {
+    typedef float store;
+    static __device__ __forceinline__ float up(store x) { return x; }
+    static __device__ __forceinline__ store down(float x) { return x; }
+};
+struct BF16 {
+    typedef uint16_t store;
+    static __device__ __forceinline__ float up(store x) { return bf16_to_f32(x); }
+    static __device__ __forceinline__ store down(float x) { return f32_to_bf16(x); }
+};
+struct F16 {
+    typedef _Float16 store;
+    static __device__ __forceinline__ float up(store x) { return (float)x; }
+    static __device__ __forceinline__ store down(float x) { return (_Float16)x; }
+};
+
+// 16 bytes of storage of type T, and what they hold.
+template <typename T>
+struct Pack16 {
+    static constexpr int N = 16 / (int)sizeof(typename T::store);
+    union {
+        uint4v raw;
+        typename T::store e[N];
+    };
+};
+
+// --------------------------------------------------------------------------
+// Muon
+// --------------------------------------------------------------------------
+
+// One matrix of a z1_muon.  X is the matrix with the smaller side first:
+// U itself, or its transpose where flip is set.  m x n are X's sides, mp x np
+// the same padded to whole tiles; the padding of every buffer holds zeros.
+struct MuonMat {
+    const void *grad;
+    float *mom;
+    float *master;
+    uint16_t *weight;
+    uint16_t *ortho;
+    int32_t rows, cols;     // of the caller's matrix
+    int32_t m, n, mp, np;
+    int32_t flip;
+    int32_t vec;            // 1: every bound pointer is 16-byte aligned
+    int64_t part0, n_part;  // its norm partials
+    _Float16 *X;            // [mp][np]  fp16 operand copy of X
+    _Float16 *Y[2];         // [np][mp]  X^T, one being read and one written
+    float *C;               // [np][mp]  X^T in fp32, the carried value
+    _Float16 *A;            // [mp][mp]
+    _Float16 *B;            // [mp][mp]
+    double lr_scale, wd_scale;
+};
+
+struct MuonTile {
+    int32_t mat, ti, tj, pad;
+};
+
+// A piece of one matrix for the elementwise pass.
+struct MuonChunk {
+    int64_t start;
+    int32_t mat, count;
+};
+
+struct MuonTables {
+    const MuonMat *mats;
+    const MuonChunk *chunks;   // elementwise pass; chunk q writes partial q
+    const MuonTile *cast;      // kCastTile square tiles of the padded X
+    const MuonTile *sym;       // GEMM tiles with ti >= tj of the mp x mp products
+    const MuonTile *full;      // GEMM tiles of the mp x np product
+    int64_t n_chunks, n_cast, n_sym, n_full;
+    double *partials;          // [n_chunks]
+    double *inv;               // [n]  1 / (|U|_F + eps)
+    int32_t n;
+    int32_t tile;              // GEMM tile side: 64, 128 or 256
+    int32_t grad_bf16;
+    float a, b, c;
+    double eps;
+};
+
+struct MuonUpdate {
+    double lr, wd;             // of the step
+    float mu;
+    int32_t nesterov;
+    double clip;               // <= 0: no clipping
+    const double *d_S;
+    int32_t step;              // 1: z1_muon_step, 0: z1_muon_orthogonalize
+};
+
+constexpr int kCastTile = 64;
+constexpr int kMuonChunk = 8192;
+
+hipError_t launch_muon(const MuonTables &t, const MuonUpdate &u, int ns_steps, hipStream_t s);
+
+// --------------------------------------------------------------------------
+// Embedding
+// --------------------------------------------------------------------------
+
+struct EmbedShape {
+    int64_t n, vocab, dim;     // ids, rows, row length
+    const void *ids;
+    int32_t id32;              // ids are int32
+    float scale;
+};
+
+constexpr int kSortBlock = 2048;   // ids one workgroup of the radix sort handles
+constexpr int kSortSmall = 8192;   // ids one workgroup sorts alone
+
+// Where z1_embed_grad's workspace holds what; offsets in bytes.
+struct EmbedWork {
+    int64_t keys[2], perm[2], hist, parts, bytes;
+    int64_t n_blocks;          // of the radix sort
+    int64_t chunk, n_chunks;   // sorted positions per chunk of the sums
+};
+
+EmbedWork embed_work(int64_t n, int64_t vocab, int64_t dim);
+
+hipError_t launch_lookup(int32_t dtype, const EmbedShape &e, const void *w, int64_t ld_w, void *out,
+                         int64_t ld_out, hipStream_t s);
+hipError_t launch_embed_grad(int32_t dtype, const EmbedShape &e, const void *dout, int64_t ld,
+                             float *dw, bool accumulate, void *work, hipStream_t s);
+
+// --------------------------------------------------------------------------
+// Losses
+// --------------------------------------------------------------------------
+
+// z1_logits as the kernels take it, and where the gradient goes.
+struct Rows {
+    int64_t n, vocab, ld, ld_d;
+    const void *x;
+    const void *y;          // targets
+    void *d;                // dlogits or null
+    int32_t y32;            // targets are int32
+    int32_t d_vec;          // a row of d sits at its x row's place mod 16 bytes
+};
+
+struct PolicyScalars {
+    float lo, hi, kl, scale;   // 1 - clip_low, 1 + clip_high
+};
+
+struct PolicyPtrs {
+    const float *old_logp, *ref_logp, *adv, *w;
+    float *token_loss, *logp;
+};
+
+hipError_t launch_logprob(int32_t dtype, const Rows &r, float *logp, float *lse, hipStream_t s);
+hipError_t launch_logprob_grad(int32_t dtype, const Rows &r, const float *lse, const float *dlogp,
+                               hipStream_t s);
+hipError_t launch_policy(int32_t dtype, const Rows &r, const PolicyPtrs &p, const PolicyScalars &k,
+                         float *loss, double scale, hipStream_t s);
+hipError_t launch_preference(const z1_preference_args &a, hipStream_t s);
+
+}  // namespace ops
+}  // namespace z1

@@ -1,0 +1,210 @@
+"""z1_embed_lookup and z1_embed_grad against the definition.
+
+The lookup multiplies in fp32 and rounds once, as torch's fp32 product and cast
+do: equal bits.  The gradient adds in fp32: n additions and the scaling are off
+by at most (n + 2) 2^-24 of the sum of magnitudes, n the number of rows that
+meet in one sum."""
+import math
+
+import pytest
+import torch
+
+from mixed_precision_zero_amd import ops as O
+
+pytestmark = pytest.mark.gpu
+DT = [torch.float32, torch.bfloat16, torch.float16]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+def make(T, V, d, dtype, seed=0, itype=torch.int64, strided=False, skew=True):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    u = torch.rand(T, generator=g, device="cuda", dtype=torch.float64)
+    ids = ((u ** 3 if skew else u) * V).long().clamp_(max=V - 1)
+    if T > 4:
+        ids[torch.rand(T, generator=g, device="cuda") < 0.1] = -1
+        ids[T // 2] = V + 5
+    wide = d + 24 if strided else d
+    w = torch.randn(V, wide, generator=g, device="cuda").to(dtype)[:, :d]
+    dout = torch.randn(T, wide, generator=g, device="cuda").to(dtype)[:, :d]
+    return ids.to(itype), w, dout
+
+
+def want_grad(ids, dout, V, scale, base=None):
+    keep = (ids >= 0) & (ids < V)
+    k = ids[keep].long()
+    x = dout[keep].double() * scale
+    out = torch.zeros(V, dout.shape[1], dtype=torch.float64, device="cuda")
+    mag = torch.zeros_like(out)
+    out.index_add_(0, k, x)
+    mag.index_add_(0, k, x.abs())
+    n = torch.bincount(k, minlength=V).double()[:, None]
+    if base is not None:
+        out += base.double()
+        mag += base.abs().double()
+    return out, (n + 2) * 2.0 ** -24 * mag + 1e-44
+
+
+def check(ids, w, dout, scale, accumulate, V):
+    T, d = dout.shape
+    out = torch.full((T, d), 7.0, device="cuda", dtype=w.dtype)
+    O.z1_embed_lookup(w, ids, out, scale=scale)
+    keep = (ids >= 0) & (ids < V)
+    ref = (w.float()[ids.long().clamp(0, V - 1)] * torch.tensor(scale, dtype=torch.float32, device="cuda")).to(w.dtype)
+    assert torch.equal(out[keep], ref[keep])
+    assert (out[ids < 0] == 0).all() and torch.isnan(out[ids >= V]).all()
+    base = torch.randn(V, d, device="cuda") if accumulate else None
+    dw = base.clone() if accumulate else torch.full((V, d), float("nan"), device="cuda")
+    ws = torch.full((O.z1_embed_grad_workspace(T, V, d),), 255, device="cuda", dtype=torch.uint8)
+    O.z1_embed_grad(ids, dout, dw, scale=scale, accumulate=accumulate, workspace=ws)
+    want, bound = want_grad(ids, dout, V, float(torch.tensor(scale, dtype=torch.float32)), base)
+    assert ((dw.double() - want).abs() <= bound).all(), float(((dw.double() - want).abs() - bound).max())
+    again = base.clone() if accumulate else torch.empty_like(dw)
+    O.z1_embed_grad(ids, dout, again, scale=scale, accumulate=accumulate, workspace=ws)
+    assert torch.equal(dw, again)
+
+
+@pytest.mark.parametrize("dtype", DT, ids=str)
+@pytest.mark.parametrize("T,V,d", [(1, 1, 1), (1, 300, 8), (2, 2, 3), (33, 256, 64), (100, 255, 7), (1000, 65536, 100),
+                                   (2047, 257, 72), (2049, 49152, 576), (8192, 1000, 24), (8193, 1000, 24),
+                                   (20000, 70000, 40), (30011, 50, 130)])
+def test_sizes(T, V, d, dtype):
+    ids, w, dout = make(T, V, d, dtype, seed=T + d)
+    check(ids, w, dout, math.sqrt(d), False, V)
+    check(ids, w, dout, 1.0, True, V)
+
+
+@pytest.mark.parametrize("dtype", DT, ids=str)
+def test_strided_rows_and_int32(dtype):
+    for T, V, d in ((500, 333, 64), (9000, 333, 61)):
+        ids, w, dout = make(T, V, d, dtype, itype=torch.int32, strided=True)
+        check(ids, w, dout, -0.5, False, V)
+        check(ids, w, dout, 3.0, True, V)
+
+
+@pytest.mark.parametrize("T", [1, 127, 128, 129, 4096, 8192, 40000])
+def test_one_id_everywhere(T):
+    ids, w, dout = make(T, 10, 48, torch.bfloat16)
+    ids.fill_(7)
+    check(ids, w, dout, 1.0, False, 10)
+
+
+@pytest.mark.parametrize("T", [64, 10000])
+def test_nothing_but_empty_positions(T):
+    ids, w, dout = make(T, 10, 48, torch.float32)
+    ids.fill_(-1)
+    dout.fill_(float("nan"))
+    check(ids, w, dout, 1.0, False, 10)
+    check(ids, w, dout, 1.0, True, 10)
+
+
+@pytest.mark.parametrize("T", [700, 12000])
+def test_empty_positions_do_not_spread(T):
+    ids, w, dout = make(T, 90, 32, torch.bfloat16)
+    dout[ids < 0] = float("nan")
+    dout[ids >= 90] = float("inf")
+    check(ids, w, dout, 1.0, False, 90)
+
+
+def test_runs_that_end_on_chunk_borders():
+    """Runs of every length around the chunk sizes, sorted and reversed."""
+    lens = [1, 15, 16, 17, 16, 16, 31, 32, 33, 64, 1, 128, 127, 129, 256, 16, 300]
+    ids = torch.cat([torch.full((n,), i, dtype=torch.long) for i, n in enumerate(lens)]).cuda()
+    for order in (ids, ids.flip(0), ids[torch.randperm(ids.numel(), generator=torch.Generator().manual_seed(1)).cuda()]):
+        for d in (8, 1024, 4096):
+            g = torch.Generator(device="cuda").manual_seed(d)
+            dout = torch.randn(order.numel(), d, generator=g, device="cuda").bfloat16()
+            w = torch.randn(len(lens) + 3, d, generator=g, device="cuda").bfloat16()
+            check(order, w, dout, 1.0, False, len(lens) + 3)
+
+
+def test_no_tokens():
+    ids = torch.zeros(0, dtype=torch.long, device="cuda")
+    dw = torch.full((50, 33), 3.0, device="cuda")
+    ws = torch.zeros(256, device="cuda", dtype=torch.uint8)
+    O.z1_embed_grad(ids, torch.zeros(0, 33, device="cuda"), dw, accumulate=True, workspace=ws)
+    assert (dw == 3).all()
+    O.z1_embed_grad(ids, torch.zeros(0, 33, device="cuda"), dw, workspace=ws)
+    assert (dw == 0).all()
+    O.z1_embed_lookup(dw, ids, torch.zeros(0, 33, device="cuda"))
+
+
+def test_unaligned_buffers():
+    ids, w, dout = make(3000, 200, 64, torch.bfloat16)
+    shift = lambda x: torch.empty(x.numel() + 8, device="cuda", dtype=x.dtype)[1:1 + x.numel()].view(x.shape).copy_(x)  # noqa: E731
+    check(ids, shift(w), shift(dout), 1.0, False, 200)
+    dw = torch.empty(200 * 64 + 8, device="cuda")[1:1 + 200 * 64].view(200, 64).fill_(float("nan"))
+    ws = torch.zeros(O.z1_embed_grad_workspace(3000, 200, 64), device="cuda", dtype=torch.uint8)
+    O.z1_embed_grad(ids, dout, dw, workspace=ws)
+    want, bound = want_grad(ids, dout, 200, 1.0)
+    assert ((dw.double() - want).abs() <= bound).all()
+
+
+def test_offsets_past_32_bits():
+    """A gradient and a table of more than 2^31 elements."""
+    V, d = (1 << 31) // 2048 + 40, 2048
+    w = torch.zeros(V, d, device="cuda", dtype=torch.bfloat16)
+    ids = torch.tensor([0, V - 1, V - 1, 5, V - 2], device="cuda")
+    w[V - 1] = 2.0
+    w[V - 2] = 3.0
+    out = torch.empty(5, d, device="cuda", dtype=torch.bfloat16)
+    O.z1_embed_lookup(w, ids, out, scale=0.5)
+    assert out[:, 0].tolist() == [0.0, 1.0, 1.0, 0.0, 1.5]
+    del w
+    dout = torch.ones(5, d, device="cuda", dtype=torch.bfloat16)
+    dw = torch.full((V, d), 9.0, device="cuda")
+    ws = torch.zeros(O.z1_embed_grad_workspace(5, V, d), device="cuda", dtype=torch.uint8)
+    O.z1_embed_grad(ids, dout, dw, workspace=ws)
+    rows = dw.sum(1)
+    assert rows[V - 1] == 2 * d and rows[V - 2] == d and rows[0] == d and rows[5] == d
+    assert int((rows != 0).sum()) == 4
+
+
+def test_other_stream_and_graph():
+    for T in (3000, 9000):
+        ids, w, dout = make(T, 500, 96, torch.bfloat16)
+        dw, ref = torch.empty(500, 96, device="cuda"), torch.empty(500, 96, device="cuda")
+        ws = torch.zeros(O.z1_embed_grad_workspace(T, 500, 96), device="cuda", dtype=torch.uint8)
+        O.z1_embed_grad(ids, dout, ref, workspace=ws)
+        torch.cuda.synchronize()
+        s = torch.cuda.Stream()
+        O.z1_embed_grad(ids, dout, dw, workspace=ws, stream=s)
+        s.synchronize()
+        assert torch.equal(dw, ref)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            O.z1_embed_grad(ids, dout, dw, workspace=ws)
+        for k in range(4):
+            dw.fill_(float("nan"))
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(dw, ref), k
+            O.z1_embed_grad(ids, dout, dw, workspace=ws)
+            torch.cuda.synchronize()
+            assert torch.equal(dw, ref), k
+
+
+def test_gradient_is_the_lookup_transposed():
+    """<dout, lookup(W)> is linear in W with slope dweight: differences of it
+    along random directions."""
+    ids, _, _ = make(200, 30, 16, torch.float32)
+    ids[ids >= 30] = -1
+    g = torch.Generator(device="cuda").manual_seed(3)
+    w, u = (torch.randn(30, 16, generator=g, device="cuda") for _ in range(2))
+    dout = torch.randn(200, 16, generator=g, device="cuda")
+    f = lambda x: (dout.double() * look(x).double()).sum()  # noqa: E731
+
+    def look(x):
+        o = torch.empty(200, 16, device="cuda")
+        O.z1_embed_lookup(x, ids, o, scale=1.5)
+        return o
+
+    dw = torch.empty(30, 16, device="cuda")
+    ws = torch.zeros(O.z1_embed_grad_workspace(200, 30, 16), device="cuda", dtype=torch.uint8)
+    O.z1_embed_grad(ids, dout, dw, scale=1.5, workspace=ws)
+    diff = (f(w + u) - f(w - u)) / 2
+    assert abs(float(diff - (dw.double() * u.double()).sum())) <= 1e-5 * float(dout.norm() * u.norm())
