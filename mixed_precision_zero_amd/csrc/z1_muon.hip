@@ -10,7 +10,7 @@
 // Every product is of the form C_ij = sum_k P_ik Q_jk with both operands
 // contiguous along k: X X^T, A A^T, and B (X^T)^T from a kept transpose Y of
 // X.  The update's epilogue writes X and Y, which costs 2 more bytes per
-// element and lets one kernel feed all three with 16-byte rows.
+// element and lets one kernel feed all three the same way.
 //
 // Numbers.  The products take fp16 operands and accumulate in fp32 on the
 // matrix cores.  X, A and B are bounded (|X| <= 1.21, |A| <= 1.46,
@@ -183,28 +183,74 @@ __global__ __launch_bounds__(256) void k_muon_cast(const MuonMat *mats, const Mu
             x[k] = (_Float16)lds[row][at + k];
             y[k] = (_Float16)lds[at + k][row];
         }
-        *reinterpret_cast<half8 *>(t.X + (int64_t)(i0 + row) * t.np + j0 + at) = x;
-        *reinterpret_cast<half8 *>(t.Y[0] + (int64_t)(j0 + row) * t.mp + i0 + at) = y;
+        *reinterpret_cast<half8 *>(t.X + panel_at(t.mp, i0 + row, j0 + at)) = x;
+        *reinterpret_cast<half8 *>(t.Y[0] + panel_at(t.np, j0 + row, i0 + at)) = y;
     }
     for (int q = threadIdx.x; q < 1024; q += 256) {
-        const int row = q >> 4, at = (q & 15) * 4;
+        // 4 rows of one column, lanes in the carry's order
+        const int block = q >> 8, i = (block >> 1) * 32 + ((q >> 6) & 3) * 8 + ((q >> 5) & 1) * 4;
+        const int j = (block & 1) * 32 + (q & 31);
         float4v y;
         for (int k = 0; k < 4; ++k)
-            y[k] = lds[at + k][row];
-        *reinterpret_cast<float4v *>(t.C + (int64_t)(j0 + row) * t.mp + i0 + at) = y;
+            y[k] = lds[i + k][j];
+        *reinterpret_cast<float4v *>(t.C + carry_at(t.np, i0 + i, j0 + j)) = y;
     }
 }
 
 enum Mode { kGram, kPoly, kUpdate, kOrtho, kStep };
 
-// C_ij = sum_k P_ik Q_jk on one T x T tile, K in steps of 64: both operands'
-// 64-wide panels come straight into LDS (16 bytes a lane, double buffered, so
-// the next panel is in flight while this one is multiplied).  A panel row is
-// 128 bytes, all 32 banks, so the 16-byte chunks of row r are stored permuted
-// by r mod 8: the 8 rows a fragment read touches at once then lie on
-// different banks.  The permutation is applied to the global address, as the
-// LDS side of the copy is fixed at 16 bytes a lane in lane order.
-template <int T, int WM, int WN, Mode MODE>
+// Transposes 4 x 4 halves across 4 lanes: lane q's column becomes row q.
+__device__ __forceinline__ half4 quad_transpose(half4 h)
+{
+    union {
+        half4 h;
+        uint32_t d[2];
+    } v;
+    v.h = h;
+    const bool odd = threadIdx.x & 1, upper = threadIdx.x & 2;
+    // with lane ^ 1: even lanes keep elements 0 and 2, odd ones 1 and 3
+    const uint32_t sel = odd ? 0x03020706u : 0x05040100u;   // bytes of {other, own}
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const uint32_t other = __builtin_amdgcn_mov_dpp(v.d[k], 0xb1, 0xf, 0xf, true);
+        v.d[k] = __builtin_amdgcn_perm(other, v.d[k], sel);
+    }
+    // with lane ^ 2: the lower two keep word 0, the upper two word 1
+    const uint32_t send = upper ? v.d[0] : v.d[1];
+    const uint32_t got = __builtin_amdgcn_mov_dpp(send, 0x4e, 0xf, 0xf, true);
+    v.d[0] = upper ? got : v.d[0];
+    v.d[1] = upper ? v.d[1] : got;
+    return v.h;
+}
+
+template <int N>
+__device__ __forceinline__ void wait_copies()
+{
+    // at most N copies of this wave outstanding, no LDS read outstanding
+    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x0070);
+}
+
+// C_ij = sum_k P_ik Q_jk on one T x T tile, one 32-deep panel after another.
+//
+// A panel's share of both operands (T x 32 halves each, contiguous) is copied
+// straight into LDS, 1 KiB a wave and instruction, into a ring of RING panels,
+// so RING - 1 panels are on their way while one is multiplied.  A row is 64
+// bytes, so four rows span the 64 banks; the 16-byte chunks of row r sit
+// permuted by (r / 4) mod 4, and the 16 lanes of a fragment read that share a
+// cycle then touch all banks once (the counters show no conflict; permuted by
+// (r / 2) mod 4, half the reads wait).  The permutation is applied to the
+// global address, as the LDS side of the copy is fixed in lane order.
+//
+// PAIRED (256 tiles, 8 waves, one workgroup a compute unit): waves w and w + 4
+// share a SIMD, and the second four run half a step behind the first, so that
+// one of the two multiplies while the other reads its fragments and issues
+// copies; two barriers a panel keep them in step.  4096 x 4096 x 4096: 110 us
+// (1250 TFLOP/s) against 139 with all waves in phase; with row-major operands
+// 121, with 64-deep panels 127.  Smaller tiles get the same effect from
+// three workgroups a compute unit; 64 tiles take two panels a step, as a step
+// of so few matrix instructions is mostly the wait for its fragments
+// (333 x 1537: 112 us against 137).
+template <int T, int WM, int WN, int PANELS, int RING, bool PAIRED, Mode MODE>
 __global__ __launch_bounds__(64 * WM * WN) void k_muon_gemm(const MuonMat *mats,
                                                             const MuonTile *tiles, int src,
                                                             float ca, float cb, float cc,
@@ -212,9 +258,10 @@ __global__ __launch_bounds__(64 * WM * WN) void k_muon_gemm(const MuonMat *mats,
 {
     constexpr int NW = WM * WN;
     constexpr int TM = T / WM / 32, TN = T / WN / 32;
-    constexpr int kLoads = T / 8 / NW;   // 1 KiB copies per wave, operand and step
+    constexpr int kLoads = T / 16 / NW;   // copies per wave, operand and panel
     static_assert(kLoads >= 1 && TM >= 1 && TN >= 1, "tile and wave grid");
-    __shared__ __align__(16) _Float16 lds[2][2 * T * 64];
+    static_assert(!PAIRED || PANELS == 1, "one panel a phase");
+    __shared__ __align__(16) _Float16 lds[RING][PANELS][2][T * 32];
 
     const MuonTile tl = tiles[blockIdx.x];
     const MuonMat &t = mats[tl.mat];
@@ -224,38 +271,44 @@ __global__ __launch_bounds__(64 * WM * WN) void k_muon_gemm(const MuonMat *mats,
     const int i0 = tl.ti * T, j0 = tl.tj * T;
 
     const _Float16 *P, *Q;
+    int64_t p_step, q_step;
     int K;
     if (MODE == kGram) {
         P = Q = t.X;
         K = t.np;
+        p_step = q_step = (int64_t)t.mp * 32;
     } else if (MODE == kPoly) {
         P = Q = t.A;
         K = t.mp;
+        p_step = q_step = (int64_t)t.mp * 32;
     } else {
         P = t.B;
         Q = t.Y[src];
         K = t.mp;
+        p_step = (int64_t)t.mp * 32;
+        q_step = (int64_t)t.np * 32;
     }
-    // both operands' rows are K elements apart; a tile's panel rows span less
-    // than 2^31 bytes (T * K * 2 with K <= 2^20 + 256)
-    const int span = T * K * 2;
-    const auto rp = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<_Float16 *>(P + (int64_t)i0 * K), 0, span, 0x00020000);
-    const auto rq = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<_Float16 *>(Q + (int64_t)j0 * K), 0, span, 0x00020000);
-    const int voff = ((lane >> 3) * K + ((lane & 7) ^ (lane >> 3)) * 8) * 2;
+    P += (int64_t)i0 * 32;
+    Q += (int64_t)j0 * 32;
+    const int voff = ((lane >> 2) * 32 + ((lane & 3) ^ ((lane >> 4) & 3)) * 8) * 2;
 
     typedef __attribute__((address_space(3))) void lds_void;
-    const auto load = [&](int b, int k) {
+    // copies the next panel; the descriptors end with the tile's share of it
+    const auto load = [&](int slot, int panel) {
+        const auto rp = __builtin_amdgcn_make_buffer_rsrc(const_cast<_Float16 *>(P), 0, T * 64, 0x00020000);
+        const auto rq = __builtin_amdgcn_make_buffer_rsrc(const_cast<_Float16 *>(Q), 0, T * 64, 0x00020000);
 #pragma unroll
         for (int q = 0; q < kLoads; ++q) {
             const int at = wave * kLoads + q;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rp, (lds_void *)&lds[b][at * 512], 16, voff,
-                                                     (at * 8 * K + k) * 2, 0, 0);
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rq, (lds_void *)&lds[b][T * 64 + at * 512],
-                                                     16, voff, (at * 8 * K + k) * 2, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rp, (lds_void *)&lds[slot][panel][0][at * 512], 16, voff,
+                                                     at * 1024, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rq, (lds_void *)&lds[slot][panel][1][at * 512], 16, voff,
+                                                     at * 1024, 0, 0);
         }
+        P += p_step;
+        Q += q_step;
     };
+    constexpr int kAhead = (RING - 2) * PANELS * 2 * kLoads;   // copies that may stay out at a wait
 
     float16v acc[TM][TN];
 #pragma unroll
@@ -267,125 +320,211 @@ __global__ __launch_bounds__(64 * WM * WN) void k_muon_gemm(const MuonMat *mats,
                 acc[i][j][r] = 0.f;
 
     const int half = lane >> 5, low = lane & 31;
-    load(0, 0);
-    const int steps = K / 64;
-    for (int k = 0; k < steps; ++k) {
-        // this panel has arrived (vmcnt 0) and every wave has read the one
-        // before it (lgkmcnt 0), whose buffer the next copy overwrites
-        __builtin_amdgcn_s_waitcnt(0x0070);
+    const auto frag = [&](const _Float16 *p, int row, int kk) {
+        return *reinterpret_cast<const half8 *>(p + row * 32 + (((kk * 2 + half) ^ ((row >> 2) & 3)) * 8));
+    };
+    const int steps = K / (32 * PANELS);
+#pragma unroll
+    for (int s = 0; s < RING - 1; ++s)
+        if (s < steps)
+#pragma unroll
+            for (int p = 0; p < PANELS; ++p)
+                load(s, p);
+    if (PAIRED) {
+        if (steps >= RING - 1)
+            wait_copies<kAhead>();
+        else
+            wait_copies<0>();
         __builtin_amdgcn_s_barrier();
+        if (wave >= NW / 2)
+            __builtin_amdgcn_s_barrier();
+    }
+    int slot = 0;
+    for (int k = 0; k < steps; ++k) {
+        const int next = slot == 0 ? RING - 1 : slot - 1;   // the slot of step k + RING - 1
+        const bool more = k + RING - 1 < steps;
+        if (!PAIRED) {
+            // panel k has arrived, and every wave has read panel k - 1, whose
+            // slot the next copy overwrites
+            if (k + RING - 2 < steps)
+                wait_copies<kAhead>();
+            else
+                wait_copies<0>();
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+            if (more)
+#pragma unroll
+                for (int p = 0; p < PANELS; ++p)
+                    load(next, p);
+        }
+        half8 a[2 * PANELS][TM], b[2 * PANELS][TN];
         asm volatile("" ::: "memory");
-        if (k + 1 < steps)
-            load((k + 1) & 1, (k + 1) * 64);
-        const _Float16 *pa = &lds[k & 1][0], *pb = &lds[k & 1][T * 64];
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-            half8 a[TM], b[TN];
+        for (int kk = 0; kk < 2 * PANELS; ++kk) {
 #pragma unroll
-            for (int i = 0; i < TM; ++i) {
-                const int r = (wm * TM + i) * 32 + low;
-                a[i] = *reinterpret_cast<const half8 *>(pa + r * 64 + (((kk * 2 + half) ^ (r & 7)) * 8));
-            }
+            for (int j = 0; j < TN; ++j)
+                b[kk][j] = frag(lds[slot][kk >> 1][1], (wn * TN + j) * 32 + low, kk & 1);
 #pragma unroll
-            for (int j = 0; j < TN; ++j) {
-                const int r = (wn * TN + j) * 32 + low;
-                b[j] = *reinterpret_cast<const half8 *>(pb + r * 64 + (((kk * 2 + half) ^ (r & 7)) * 8));
-            }
+            for (int i = 0; i < TM; ++i)
+                a[kk][i] = frag(lds[slot][kk >> 1][0], (wm * TM + i) * 32 + low, kk & 1);
+        }
+        if (PAIRED) {
+            // the slot being filled was last read in panel k - 1, by both
+            // halves before the barrier that ended their reads of it
+            if (more)
+                load(next, 0);
+            asm volatile("" ::: "memory");
+            // panel k + 1 has arrived once every wave is past this barrier
+            if (more)
+                wait_copies<kAhead>();
+            else
+                wait_copies<0>();
+            __builtin_amdgcn_s_barrier();
+            __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int kk = 0; kk < 2 * PANELS; ++kk)
 #pragma unroll
             for (int i = 0; i < TM; ++i)
 #pragma unroll
                 for (int j = 0; j < TN; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a[i], b[j], acc[i][j], 0, 0, 0);
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a[kk][i], b[kk][j], acc[i][j], 0, 0, 0);
+        if (PAIRED) {
+            __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_s_barrier();
+            __builtin_amdgcn_sched_barrier(0);
         }
         asm volatile("" ::: "memory");
+        slot = slot + 1 == RING ? 0 : slot + 1;
     }
+    if (PAIRED && wave < NW / 2)
+        __builtin_amdgcn_s_barrier();   // as many as the second four
 
     // A lane holds, of each 32 x 32 block, column `low` and rows
-    // 8 g + 4 half + (0..3) for g = 0..3.
+    // 8 g + 4 half + (0..3) for g = 0..3: 8 bytes of the transposed operand.
+    // Four lanes' 4 x 4 halves are transposed for the 8 bytes of the other.
+    // What a block reads is read before any of it is written: a load behind a
+    // store to what may be the same place waits for it (20 us a 256 tile).
     const double decay = 1.0 - u.lr * u.wd * t.wd_scale, step = u.lr * t.lr_scale;
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
+        const int64_t bi = i0 / 32 + wm * TM + i;
+        if (MODE == kGram || MODE == kPoly) {
+            half4 x[TN][4];
+            if (MODE == kPoly)
 #pragma unroll
-        for (int j = 0; j < TN; ++j) {
-            const int jj = j0 + (wn * TN + j) * 32 + low;
+                for (int j = 0; j < TN; ++j)
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const int ii = i0 + (wm * TM + i) * 32 + 8 * g + 4 * half;
-                float v[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    v[k] = acc[i][j][4 * g + k] * kUnscale;
-                if (MODE == kGram || MODE == kPoly) {
-                    _Float16 *D = MODE == kGram ? t.A : t.B;
-                    if (MODE == kPoly) {
-                        const half4 x = *reinterpret_cast<const half4 *>(t.A + (int64_t)jj * t.mp + ii);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            v[k] = fmaf(cc, v[k], cb * (float)x[k]);
+                    for (int g = 0; g < 4; ++g) {
+                        const int64_t bj = j0 / 32 + wn * TN + j;
+                        x[j][g] = *reinterpret_cast<const half4 *>(
+                            t.A + (bi * t.mp + bj * 32 + low) * 32 + half * 4 + g * 8);
                     }
+            _Float16 *D = MODE == kGram ? t.A : t.B;
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+                const int64_t bj = j0 / 32 + wn * TN + j;
+                _Float16 *at = D + (bi * t.mp + bj * 32 + low) * 32 + half * 4;
+                _Float16 *mirror = D + (bj * t.mp + bi * 32 + half * 4 + (lane & 3)) * 32 + (low & ~3);
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
                     half4 h;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        h[k] = (_Float16)v[k];
-                    *reinterpret_cast<half4 *>(D + (int64_t)jj * t.mp + ii) = h;
+                    for (int k = 0; k < 4; ++k) {
+                        float v = acc[i][j][4 * g + k] * kUnscale;
+                        if (MODE == kPoly)
+                            v = fmaf(cc, v, cb * (float)x[j][g][k]);
+                        h[k] = (_Float16)v;
+                    }
+                    *reinterpret_cast<half4 *>(at + g * 8) = h;
                     if (tl.ti != tl.tj)
+                        *reinterpret_cast<half4 *>(mirror + g * 256) = quad_transpose(h);
+                }
+            }
+        } else {
+            float4v x[TN][4];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            D[(int64_t)(ii + k) * t.mp + jj] = h[k];
-                } else {
-                    float4v *cp = reinterpret_cast<float4v *>(t.C + (int64_t)jj * t.mp + ii);
-                    const float4v x = *cp;
+            for (int j = 0; j < TN; ++j)
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const int64_t bj = j0 / 32 + wn * TN + j;
+                    x[j][g] = *reinterpret_cast<const float4v *>(
+                        t.C + (bi * (t.np >> 5) + bj) * 1024 + lane * 4 + g * 256);
+                }
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+#pragma unroll
+                for (int g = 0; g < 4; ++g)
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        v[k] = fmaf(ca, x[k], v[k]);
-                    if (MODE == kUpdate) {
-                        float4v y;
+                        x[j][g][k] = fmaf(ca, x[j][g][k], acc[i][j][4 * g + k] * kUnscale);
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+                const int64_t bj = j0 / 32 + wn * TN + j;
+                if (MODE == kUpdate) {
+                    float *carry = t.C + (bi * (t.np >> 5) + bj) * 1024 + lane * 4;
+                    _Float16 *yt = t.Y[src ^ 1] + (bi * t.np + bj * 32 + low) * 32 + half * 4;
+                    _Float16 *xt = t.X + (bj * t.mp + bi * 32 + half * 4 + (lane & 3)) * 32 + (low & ~3);
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
                         half4 h;
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            y[k] = v[k];
-                            h[k] = (_Float16)v[k];
-                            t.X[(int64_t)(ii + k) * t.np + jj] = h[k];
-                        }
-                        *cp = y;
-                        *reinterpret_cast<half4 *>(t.Y[src ^ 1] + (int64_t)jj * t.mp + ii) = h;
-                    } else {
+                        for (int k = 0; k < 4; ++k)
+                            h[k] = (_Float16)x[j][g][k];
+                        *reinterpret_cast<float4v *>(carry + g * 256) = x[j][g];
+                        *reinterpret_cast<half4 *>(yt + g * 8) = h;
+                        *reinterpret_cast<half4 *>(xt + g * 256) = quad_transpose(h);
+                    }
+                } else {
+                    // element (i, j) of X sits at i * si + j * sj of the caller's matrix
+                    const int64_t si = t.flip ? 1 : t.cols, sj = t.flip ? t.cols : 1;
+                    const int64_t ii = bi * 32 + half * 4, jj = bj * 32 + low;
+                    float w[4][4];
+#pragma unroll
+                    for (int g = 0; g < 4; ++g)
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            if (ii + k >= t.m || jj >= t.n)
-                                continue;
-                            const int64_t e = t.flip ? (int64_t)jj * t.cols + ii + k
-                                                     : (int64_t)(ii + k) * t.cols + jj;
-                            const float o = v[k] * kUnscale;
-                            if (MODE == kOrtho) {
-                                t.ortho[e] = f32_to_bf16(o);
-                            } else {
-                                const float w = (float)((double)t.master[e] * decay - step * (double)o);
-                                t.master[e] = w;
-                                t.weight[e] = f32_to_bf16(w);
+                            const int64_t r = ii + 8 * g + k;
+                            w[g][k] = x[j][g][k] * kUnscale;
+                            if (MODE == kStep) {
+                                const float o = w[g][k];
+                                w[g][k] = 0.f;
+                                if (r < t.m && jj < t.n)
+                                    w[g][k] = (float)((double)t.master[r * si + jj * sj] * decay - step * (double)o);
                             }
                         }
-                    }
+                    uint16_t *out = MODE == kOrtho ? t.ortho : t.weight;
+#pragma unroll
+                    for (int g = 0; g < 4; ++g)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int64_t r = ii + 8 * g + k, e = r * si + jj * sj;
+                            if (r < t.m && jj < t.n) {
+                                if (MODE == kStep)
+                                    t.master[e] = w[g][k];
+                                out[e] = f32_to_bf16(w[g][k]);
+                            }
+                        }
                 }
             }
         }
     }
 }
 
-template <int T, int WM, int WN>
+template <int T, int WM, int WN, int PANELS, int RING, bool PAIRED>
 void iterate(const MuonTables &t, const MuonUpdate &u, int ns_steps, hipStream_t s)
 {
     constexpr int B = 64 * WM * WN;
     for (int k = 0; k < ns_steps; ++k) {
         const int src = k & 1;
-        k_muon_gemm<T, WM, WN, kGram><<<(uint32_t)t.n_sym, B, 0, s>>>(t.mats, t.sym, src, t.a, t.b, t.c, u);
-        k_muon_gemm<T, WM, WN, kPoly><<<(uint32_t)t.n_sym, B, 0, s>>>(t.mats, t.sym, src, t.a, t.b, t.c, u);
+        k_muon_gemm<T, WM, WN, PANELS, RING, PAIRED, kGram><<<(uint32_t)t.n_sym, B, 0, s>>>(t.mats, t.sym, src, t.a, t.b, t.c, u);
+        k_muon_gemm<T, WM, WN, PANELS, RING, PAIRED, kPoly><<<(uint32_t)t.n_sym, B, 0, s>>>(t.mats, t.sym, src, t.a, t.b, t.c, u);
         if (k + 1 < ns_steps)
-            k_muon_gemm<T, WM, WN, kUpdate><<<(uint32_t)t.n_full, B, 0, s>>>(t.mats, t.full, src, t.a, t.b, t.c, u);
+            k_muon_gemm<T, WM, WN, PANELS, RING, PAIRED, kUpdate><<<(uint32_t)t.n_full, B, 0, s>>>(t.mats, t.full, src, t.a, t.b, t.c, u);
         else if (u.step)
-            k_muon_gemm<T, WM, WN, kStep><<<(uint32_t)t.n_full, B, 0, s>>>(t.mats, t.full, src, t.a, t.b, t.c, u);
+            k_muon_gemm<T, WM, WN, PANELS, RING, PAIRED, kStep><<<(uint32_t)t.n_full, B, 0, s>>>(t.mats, t.full, src, t.a, t.b, t.c, u);
         else
-            k_muon_gemm<T, WM, WN, kOrtho><<<(uint32_t)t.n_full, B, 0, s>>>(t.mats, t.full, src, t.a, t.b, t.c, u);
+            k_muon_gemm<T, WM, WN, PANELS, RING, PAIRED, kOrtho><<<(uint32_t)t.n_full, B, 0, s>>>(t.mats, t.full, src, t.a, t.b, t.c, u);
     }
 }
 
@@ -408,11 +547,11 @@ hipError_t launch_muon(const MuonTables &t, const MuonUpdate &u, int ns_steps, h
     else
         u.step ? first<false, true>(t, u, s) : first<false, false>(t, u, s);
     if (t.tile == 256)
-        iterate<256, 2, 4>(t, u, ns_steps, s);
+        iterate<256, 2, 4, 1, 4, true>(t, u, ns_steps, s);
     else if (t.tile == 128)
-        iterate<128, 2, 2>(t, u, ns_steps, s);
+        iterate<128, 2, 2, 1, 3, false>(t, u, ns_steps, s);
     else
-        iterate<64, 2, 2>(t, u, ns_steps, s);
+        iterate<64, 2, 2, 2, 3, false>(t, u, ns_steps, s);
     return hipGetLastError();
 }
 

@@ -131,32 +131,49 @@ bool coefficients_ok(const z1_muon_bind *b)
 
 int64_t pad_to(int64_t x, int64_t q) { return (x + q - 1) / q * q; }
 
-// The tile side the products run with.
+// The tile side the products run with: the one with the smallest estimate of
+// a step's time.  A product of `tiles` tiles of `panels` 32-deep panels takes
+//   fixed + panels * max(alone, ceil(tiles / 256) * shared)   microseconds,
+// `alone` a tile's time per panel when it has a compute unit for itself and
+// `shared` its share of a full one; the constants are fitted to these times
+// of whole calls (us, 64 / 128 / 256 tiles): 1 x 64 x 256 62 / 111 / 252,
+// 8 x 576 x 1536 260 / 319 / 544, 4 x 1024^2 249 / 298 / 523, 1 x 2048^2 388 /
+// 441 / 777, 2 x 2048 x 8192 2403 / 1864 / 2029, 4 x 2048^2 1263 / 1043 /
+// 1023, 24 x 2048^2 7936 / 6364 / 5551, 1 x 4096 x 11008 5946 / 4106 / 3651;
+// the estimate picks the fastest of the three in all of them.
 int pick_tile(int32_t n, const int64_t *rows, const int64_t *cols)
 {
 #ifdef Z1_MUON_TILE
     return Z1_MUON_TILE;   // for measuring one side against another
 #endif
+    static const struct {
+        int side;
+        double fixed, alone, shared;
+    } kTiles[3] = {{64, 2.5, 0.16, 0.112}, {128, 6.0, 0.32, 0.327}, {256, 13.0, 0.6, 0.88}};
+    int tile = 0;
     double best = 0.0;
-    int tile = 64;
-    const int sides[3] = {64, 128, 256};
-    const int slots[3] = {1024, 512, 256};
-    const double step[3] = {0.25, 0.45, 1.0};
-    for (int c = 0; c < 3; ++c) {
-        double tiles = 0.0, work = 0.0;
-        const int T = sides[c];
+    for (const auto &c : kTiles) {
+        // gram, polynomial and update product: tiles, tiles * panels, longest
+        double tiles[3] = {}, work[3] = {}, deep[3] = {};
         for (int32_t i = 0; i < n; ++i) {
-            const double m = (double)pad_to(std::min(rows[i], cols[i]), T);
-            const double w = (double)pad_to(std::max(rows[i], cols[i]), T);
-            const double q = m / T, f = q * (w / T), sy = q * (q + 1) / 2;
-            tiles += f;
-            work += f * m + sy * (w + m);
+            const double m = (double)pad_to(std::min(rows[i], cols[i]), c.side);
+            const double w = (double)pad_to(std::max(rows[i], cols[i]), c.side);
+            const double q = m / c.side;
+            const double t[3] = {q * (q + 1) / 2, q * (q + 1) / 2, q * (w / c.side)};
+            const double k[3] = {w / 32, m / 32, m / 32};
+            for (int p = 0; p < 3; ++p) {
+                tiles[p] += t[p];
+                work[p] += t[p] * k[p];
+                deep[p] = std::max(deep[p], k[p]);
+            }
         }
-        const double waves = ceil(tiles / slots[c]) / (tiles / slots[c]);
-        const double cost = work / slots[c] * step[c] * waves;
-        if (c == 0 || cost < best) {
+        double cost = 0.0;
+        for (int p = 0; p < 3 && n > 0; ++p)
+            cost += c.fixed + std::max(deep[p] * c.alone,
+                                       ceil(tiles[p] / 256.0) * (work[p] / tiles[p]) * c.shared);
+        if (tile == 0 || cost < best) {
             best = cost;
-            tile = T;
+            tile = c.side;
         }
     }
     return tile;

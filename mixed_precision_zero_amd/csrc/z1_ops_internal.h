@@ -83,11 +83,11 @@ struct MuonMat {
     int32_t flip;
     int32_t vec;            // 1: every bound pointer is 16-byte aligned
     int64_t part0, n_part;  // its norm partials
-    _Float16 *X;            // [mp][np]  fp16 operand copy of X
-    _Float16 *Y[2];         // [np][mp]  X^T, one being read and one written
-    float *C;               // [np][mp]  X^T in fp32, the carried value
-    _Float16 *A;            // [mp][mp]
-    _Float16 *B;            // [mp][mp]
+    // operands, panel-major (see panel_at)
+    _Float16 *X;            // mp rows, np deep: the operand copy of X
+    _Float16 *Y[2];         // np rows, mp deep: of X^T, one being read and one written
+    _Float16 *A, *B;        // mp rows, mp deep
+    float *C;               // the carried X in fp32 (see carry_at)
     double lr_scale, wd_scale;
 };
 
@@ -125,6 +125,21 @@ struct MuonUpdate {
     const double *d_S;
     int32_t step;              // 1: z1_muon_step, 0: z1_muon_orthogonalize
 };
+
+// Element (row, k) of an fp16 operand with `rows` rows: panels of 32 along k,
+// each [rows][32], so that a tile's share of a panel is one contiguous piece.
+__host__ __device__ __forceinline__ int64_t panel_at(int64_t rows, int64_t row, int64_t k)
+{
+    return ((k >> 5) * rows + row) * 32 + (k & 31);
+}
+
+// Element (i, j) of the fp32 carry of X (np columns): blocks of 32 x 32 in the
+// order in which the matrix instruction's lanes hold them, 16 bytes a lane.
+__host__ __device__ __forceinline__ int64_t carry_at(int64_t np, int64_t i, int64_t j)
+{
+    const int64_t block = (i >> 5) * (np >> 5) + (j >> 5);
+    return block * 1024 + ((i & 31) >> 3) * 256 + (((i >> 2) & 1) * 32 + (j & 31)) * 4 + (i & 3);
+}
 
 constexpr int kCastTile = 64;
 constexpr int kMuonChunk = 8192;
