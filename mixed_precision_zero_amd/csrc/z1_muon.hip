@@ -230,6 +230,84 @@ __device__ __forceinline__ void wait_copies()
     __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x0070);
 }
 
+// The caller's outputs of one 32 x 32 block of the last X, held as the matrix
+// instruction leaves it: column `low`, rows 8 g + 4 half + k.  Element (i, j)
+// of X sits at i * si + j * sj of the caller's matrix.  A whole block of
+// 16-byte aligned rows is written 8 or 16 bytes a lane without a test per
+// element (4 x 2048 x 2048: 274 us for this product with the tests, 86 for
+// one that writes no outputs).
+template <Mode MODE>
+__device__ __forceinline__ void put_block(const MuonMat &t, const MuonUpdate &u, int64_t i0, int64_t j0,
+                                          const float4v (&x)[4])
+{
+    const int lane = threadIdx.x & 63, half = lane >> 5, low = lane & 31;
+    const double decay = 1.0 - u.lr * u.wd * t.wd_scale, step = u.lr * t.lr_scale;
+    uint16_t *out = MODE == kOrtho ? t.ortho : t.weight;
+    const auto fresh = [&](float o, float old) {
+        return MODE == kOrtho ? o : (float)((double)old * decay - step * (double)o);
+    };
+    const int64_t ii = i0 + half * 4, jj = j0 + low;
+    if (t.vec4 && i0 + 32 <= t.m && j0 + 32 <= t.n) {
+        float4v w[4];
+        if (t.flip) {
+            const int64_t at = jj * t.cols + ii;
+            if (MODE == kStep)
+#pragma unroll
+                for (int g = 0; g < 4; ++g)
+                    w[g] = *reinterpret_cast<const float4v *>(t.master + at + 8 * g);
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                half4 h;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    w[g][k] = fresh(x[g][k] * kUnscale, w[g][k]);
+                    h[k] = __builtin_bit_cast(_Float16, f32_to_bf16(w[g][k]));
+                }
+                if (MODE == kStep)
+                    *reinterpret_cast<float4v *>(t.master + at + 8 * g) = w[g];
+                *reinterpret_cast<half4 *>(out + at + 8 * g) = h;
+            }
+        } else {
+            float *m = t.master + ii * t.cols + jj;
+            uint16_t *o = out + (ii + (lane & 3)) * t.cols + (jj & ~3);
+            if (MODE == kStep)
+#pragma unroll
+                for (int g = 0; g < 4; ++g)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        w[g][k] = m[(int64_t)(8 * g + k) * t.cols];
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                half4 h;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    w[g][k] = fresh(x[g][k] * kUnscale, w[g][k]);
+                    h[k] = __builtin_bit_cast(_Float16, f32_to_bf16(w[g][k]));
+                    if (MODE == kStep)
+                        m[(int64_t)(8 * g + k) * t.cols] = w[g][k];
+                }
+                *reinterpret_cast<half4 *>(o + (int64_t)(8 * g) * t.cols) = quad_transpose(h);
+            }
+        }
+        return;
+    }
+    const int64_t si = t.flip ? 1 : t.cols, sj = t.flip ? t.cols : 1;
+    if (jj < t.n) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int64_t r = ii + 8 * g + k, e = r * si + jj * sj;
+                if (r < t.m) {
+                    const float w = fresh(x[g][k] * kUnscale, MODE == kStep ? t.master[e] : 0.f);
+                    if (MODE == kStep)
+                        t.master[e] = w;
+                    out[e] = f32_to_bf16(w);
+                }
+            }
+    }
+}
+
 // C_ij = sum_k P_ik Q_jk on one T x T tile, one 32-deep panel after another.
 //
 // A panel's share of both operands (T x 32 halves each, contiguous) is copied
@@ -405,7 +483,6 @@ __global__ __launch_bounds__(64 * WM * WN) void k_muon_gemm(const MuonMat *mats,
     // Four lanes' 4 x 4 halves are transposed for the 8 bytes of the other.
     // What a block reads is read before any of it is written: a load behind a
     // store to what may be the same place waits for it (20 us a 256 tile).
-    const double decay = 1.0 - u.lr * u.wd * t.wd_scale, step = u.lr * t.lr_scale;
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
         const int64_t bi = i0 / 32 + wm * TM + i;
@@ -476,35 +553,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_muon_gemm(const MuonMat *mats,
                         *reinterpret_cast<half4 *>(xt + g * 256) = quad_transpose(h);
                     }
                 } else {
-                    // element (i, j) of X sits at i * si + j * sj of the caller's matrix
-                    const int64_t si = t.flip ? 1 : t.cols, sj = t.flip ? t.cols : 1;
-                    const int64_t ii = bi * 32 + half * 4, jj = bj * 32 + low;
-                    float w[4][4];
-#pragma unroll
-                    for (int g = 0; g < 4; ++g)
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const int64_t r = ii + 8 * g + k;
-                            w[g][k] = x[j][g][k] * kUnscale;
-                            if (MODE == kStep) {
-                                const float o = w[g][k];
-                                w[g][k] = 0.f;
-                                if (r < t.m && jj < t.n)
-                                    w[g][k] = (float)((double)t.master[r * si + jj * sj] * decay - step * (double)o);
-                            }
-                        }
-                    uint16_t *out = MODE == kOrtho ? t.ortho : t.weight;
-#pragma unroll
-                    for (int g = 0; g < 4; ++g)
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const int64_t r = ii + 8 * g + k, e = r * si + jj * sj;
-                            if (r < t.m && jj < t.n) {
-                                if (MODE == kStep)
-                                    t.master[e] = w[g][k];
-                                out[e] = f32_to_bf16(w[g][k]);
-                            }
-                        }
+                    put_block<MODE>(t, u, bi * 32, bj * 32, x[j]);
                 }
             }
         }

@@ -270,6 +270,7 @@ z1_status muon_create(z1_muon **out, const z1_muon_bind *b, z1_stream stream)
         }
         if (m->can_ortho)
             q.ortho = static_cast<uint16_t *>(b->ortho[i]);
+        q.vec4 = q.cols % 4 == 0 && aligned(q.master, 16) && aligned(q.weight, 8) && aligned(q.ortho, 8);
         q.lr_scale = b->lr_scale ? b->lr_scale[i] : 1.0;
         q.wd_scale = b->wd_scale ? b->wd_scale[i] : 1.0;
         const int64_t numel = (int64_t)q.rows * q.cols;

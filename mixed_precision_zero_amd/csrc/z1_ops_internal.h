@@ -81,7 +81,8 @@ struct MuonMat {
     int32_t rows, cols;     // of the caller's matrix
     int32_t m, n, mp, np;
     int32_t flip;
-    int32_t vec;            // 1: every bound pointer is 16-byte aligned
+    int32_t vec;            // 1: grad and momentum are 16-byte aligned
+    int32_t vec4;           // 1: so are the rows of master, weight and ortho (8 bytes for bf16)
     int64_t part0, n_part;  // its norm partials
     // operands, panel-major (see panel_at)
     _Float16 *X;            // mp rows, np deep: the operand copy of X
