@@ -51,6 +51,7 @@ struct Flat {
 template <typename T, int N>
 struct Vec {
     float f[N];
+    template <bool STREAM = false>
     __device__ __forceinline__ void load(const void *base, int64_t i)
     {
         const typename T::store *p = static_cast<const typename T::store *>(base) + i;
@@ -58,12 +59,15 @@ struct Vec {
             f[0] = T::up(p[0]);
         } else {
             Pack16<T> q;
-            q.raw = *reinterpret_cast<const uint4v *>(p);
+            q.raw = STREAM ? __builtin_nontemporal_load(reinterpret_cast<const uint4v *>(p))
+                           : *reinterpret_cast<const uint4v *>(p);
 #pragma unroll
             for (int k = 0; k < N; ++k)
                 f[k] = T::up(q.e[k]);
         }
     }
+    // STREAM: more than the caches hold is being written
+    template <bool STREAM>
     __device__ __forceinline__ void store(void *base, int64_t i) const
     {
         typename T::store *p = static_cast<typename T::store *>(base) + i;
@@ -74,7 +78,10 @@ struct Vec {
 #pragma unroll
             for (int k = 0; k < N; ++k)
                 q.e[k] = T::down(f[k]);
-            *reinterpret_cast<uint4v *>(p) = q.raw;
+            if (STREAM)
+                __builtin_nontemporal_store(q.raw, reinterpret_cast<uint4v *>(p));
+            else
+                *reinterpret_cast<uint4v *>(p) = q.raw;
         }
     }
     // as fp32 rows
@@ -105,26 +112,39 @@ struct Vec {
     }
 };
 
-template <typename T, int N>
+// R positions a lane, whose ids, rows and results are each in flight together.
+template <typename T, int N, int R>
 __global__ __launch_bounds__(256) void k_lookup(EmbedShape e, const void *w, int64_t ld_w, void *out,
                                                 int64_t ld_out, int32_t per, int64_t row0, int64_t row1)
 {
     const Flat at(per, row0);
     if (at.row >= row1)
         return;
-    const int64_t id = id_at(e, at.row);
-    Vec<T, N> x;
-    if (id >= 0 && id < e.vocab) {
-        x.load(w, id * ld_w + (int64_t)at.vec * N);
+    const int64_t first = at.row * R, col = (int64_t)at.vec * N;
+    int64_t id[R];
+    Vec<T, N> x[R];
 #pragma unroll
-        for (int k = 0; k < N; ++k)
-            x.f[k] *= e.scale;
-    } else {
+    for (int q = 0; q < R; ++q)
+        id[q] = first + q < e.n ? id_at(e, first + q) : -1;
 #pragma unroll
-        for (int k = 0; k < N; ++k)
-            x.f[k] = id < 0 ? 0.f : __builtin_nanf("");
+    for (int q = 0; q < R; ++q) {
+        if (id[q] >= 0 && id[q] < e.vocab) {
+            x[q].load(w, id[q] * ld_w + col);
+        } else {
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+                x[q].f[k] = id[q] < 0 ? 0.f : __builtin_nanf("");
+        }
     }
-    x.store(out, at.row * ld_out + (int64_t)at.vec * N);
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+        if (first + q >= e.n)
+            break;
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            x[q].f[k] *= e.scale;
+        x[q].template store<(R > 1)>(out, (first + q) * ld_out + col);
+    }
 }
 
 // ------------------------------------------------------------------ sorting
@@ -136,8 +156,9 @@ __device__ __forceinline__ void fill_zero(float *p, int64_t n, int64_t block, in
     const int64_t step = blocks * blockDim.x, first = block * blockDim.x + threadIdx.x;
     if (reinterpret_cast<uintptr_t>(p) % 16 == 0) {
         float4v *q = reinterpret_cast<float4v *>(p);
+#pragma unroll 4
         for (int64_t i = first; i < n / 4; i += step)
-            q[i] = float4v{0.f, 0.f, 0.f, 0.f};
+            __builtin_nontemporal_store(float4v{0.f, 0.f, 0.f, 0.f}, q + i);
         for (int64_t i = n / 4 * 4 + first; i < n; i += step)
             p[i] = 0.f;
     } else {
@@ -185,33 +206,45 @@ __device__ __forceinline__ void place_wave(volatile uint32_t *next, int64_t firs
     }
 }
 
+// Exclusive prefix of one value a thread over the first 256 threads; every
+// thread of the workgroup calls it.
+__device__ __forceinline__ uint32_t prefix_256(uint32_t x, uint32_t *tmp)
+{
+    const int t = threadIdx.x, lane = t & 63;
+    uint32_t up = x;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const uint32_t y = __shfl_up(up, o);
+        if (lane >= o)
+            up += y;
+    }
+    if (t < 256 && lane == 63)
+        tmp[t >> 6] = up;
+    __syncthreads();
+    uint32_t before = up - x;
+    for (int w = 0; w < (t >> 6) && w < 4; ++w)
+        before += tmp[w];
+    return before;
+}
+
 // Exclusive prefix, over digits and then waves, of cnt[wave][256]: position of
-// each wave's first item of each digit.  1024 threads (16 waves) or 256 (4).
+// each wave's first item of each digit.
 template <int WAVES>
 __device__ __forceinline__ void prefix_counts(uint32_t (*cnt)[256], uint32_t *tmp)
 {
     const int t = threadIdx.x;
     uint32_t total = 0;
     if (t < 256) {
+#pragma unroll
         for (int w = 0; w < WAVES; ++w) {
             const uint32_t c = cnt[w][t];
             cnt[w][t] = total;
             total += c;
         }
-        tmp[t] = total;
     }
-    __syncthreads();
-    for (int o = 1; o < 256; o <<= 1) {
-        uint32_t add = 0;
-        if (t < 256 && t >= o)
-            add = tmp[t - o];
-        __syncthreads();
-        if (t < 256)
-            tmp[t] += add;
-        __syncthreads();
-    }
+    const uint32_t before = prefix_256(total, tmp);
     if (t < 256) {
-        const uint32_t before = tmp[t] - total;
+#pragma unroll
         for (int w = 0; w < WAVES; ++w)
             cnt[w][t] += before;
     }
@@ -226,7 +259,7 @@ __global__ __launch_bounds__(1024) void k_sort_small(EmbedShape e, int passes, u
     __shared__ uint32_t key[2][kSortSmall];
     __shared__ uint16_t pos[2][kSortSmall];
     __shared__ uint32_t cnt[16][256];
-    __shared__ uint32_t tmp[256];
+    __shared__ uint32_t tmp[4];
     if (blockIdx.x > 0) {
         fill_zero(dw, dw_elems, blockIdx.x - 1, gridDim.x - 1);
         return;
@@ -265,11 +298,17 @@ __global__ __launch_bounds__(1024) void k_sort_small(EmbedShape e, int passes, u
     }
 }
 
-// One 8-bit pass over many workgroups: counts, their prefix, placement.
+// One 8-bit pass over many workgroups: hist[block][digit], then placement.  In
+// the first pass the workgroups after the last block clear dW.
 __global__ __launch_bounds__(256) void k_sort_count(EmbedShape e, const uint32_t *keys, int shift,
-                                                    uint32_t *hist, int64_t n_blocks)
+                                                    uint32_t *hist, int64_t n_blocks, float *dw,
+                                                    int64_t dw_elems)
 {
     __shared__ uint32_t cnt[256];
+    if (blockIdx.x >= n_blocks) {
+        fill_zero(dw, dw_elems, blockIdx.x - n_blocks, gridDim.x - n_blocks);
+        return;
+    }
     cnt[threadIdx.x] = 0u;
     __syncthreads();
     const int64_t first = (int64_t)blockIdx.x * kSortBlock;
@@ -280,55 +319,39 @@ __global__ __launch_bounds__(256) void k_sort_count(EmbedShape e, const uint32_t
             atomicAdd(&cnt[((keys ? keys[i] : key_at(e, i)) >> shift) & 255u], 1u);
     }
     __syncthreads();
-    hist[threadIdx.x * n_blocks + blockIdx.x] = cnt[threadIdx.x];
+    hist[(int64_t)blockIdx.x * 256 + threadIdx.x] = cnt[threadIdx.x];
 }
 
-// Exclusive prefix of hist in place, by one workgroup; the others clear dW.
-__global__ __launch_bounds__(1024) void k_sort_prefix(uint32_t *hist, int64_t n, float *dw,
-                                                      int64_t dw_elems)
+// Many blocks: hist[block][digit] becomes the digit's count in the blocks
+// before, and hist[n_blocks][digit] its count in all, by one workgroup whose
+// four groups of 256 threads take a quarter of the blocks each.
+__global__ __launch_bounds__(1024) void k_sort_prefix(uint32_t *hist, int64_t n_blocks)
 {
-    __shared__ uint32_t waves[16];
-    if (blockIdx.x > 0) {
-        fill_zero(dw, dw_elems, blockIdx.x - 1, gridDim.x - 1);
-        return;
+    __shared__ uint32_t part[4][256];
+    const int d = threadIdx.x & 255, group = threadIdx.x >> 8;
+    const int64_t lo = n_blocks * group / 4, hi = n_blocks * (group + 1) / 4;
+    uint32_t sum = 0;
+#pragma unroll 16
+    for (int64_t b = lo; b < hi; ++b)
+        sum += hist[b * 256 + d];
+    part[group][d] = sum;
+    __syncthreads();
+    uint32_t at = 0;
+    for (int g = 0; g < group; ++g)
+        at += part[g][d];
+#pragma unroll 16
+    for (int64_t b = lo; b < hi; ++b) {
+        const uint32_t c = hist[b * 256 + d];
+        hist[b * 256 + d] = at;
+        at += c;
     }
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    uint32_t carry = 0;
-    for (int64_t at = 0; at < n; at += 4096) {
-        const int64_t i = at + (int64_t)threadIdx.x * 4;
-        uint32_t v[4], sum = 0;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            v[k] = i + k < n ? hist[i + k] : 0u;
-            sum += v[k];
-        }
-        uint32_t up = sum;
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-            const uint32_t x = __shfl_up(up, o);
-            if (lane >= o)
-                up += x;
-        }
-        if (lane == 63)
-            waves[wave] = up;
-        __syncthreads();
-        uint32_t before = carry, all = 0;
-        for (int w = 0; w < 16; ++w) {
-            if (w < wave)
-                before += waves[w];
-            all += waves[w];
-        }
-        before += up - sum;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            if (i + k < n)
-                hist[i + k] = before;
-            before += v[k];
-        }
-        carry += all;
-        __syncthreads();
-    }
+    if (group == 3)
+        hist[n_blocks * 256 + d] = at;
 }
+
+// Up to this many blocks, each workgroup of the placement adds up the counts
+// of the others by itself: 64 blocks 3 us, where a kernel of its own took 11.
+constexpr int64_t kSortInline = 128;
 
 __global__ __launch_bounds__(256) void k_sort_place(EmbedShape e, const uint32_t *keys,
                                                     const uint32_t *perm, int shift,
@@ -336,6 +359,7 @@ __global__ __launch_bounds__(256) void k_sort_place(EmbedShape e, const uint32_t
                                                     uint32_t *keys_out, uint32_t *perm_out)
 {
     __shared__ uint32_t cnt[4][256];
+    __shared__ uint32_t tmp[4];
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
 #pragma unroll
     for (int w = 0; w < 4; ++w)
@@ -350,8 +374,19 @@ __global__ __launch_bounds__(256) void k_sort_place(EmbedShape e, const uint32_t
         if (i < e.n)
             atomicAdd(&cnt[wave][(key_of(i) >> shift) & 255u], 1u);
     }
-    __syncthreads();
-    uint32_t at = hist[threadIdx.x * n_blocks + blockIdx.x];
+    uint32_t all = 0, at = 0;
+    if (n_blocks <= kSortInline) {
+#pragma unroll 16
+        for (int64_t b = 0; b < n_blocks; ++b) {
+            const uint32_t c = hist[b * 256 + threadIdx.x];
+            all += c;
+            at += b < blockIdx.x ? c : 0u;
+        }
+    } else {
+        all = hist[n_blocks * 256 + threadIdx.x];
+        at = hist[(int64_t)blockIdx.x * 256 + threadIdx.x];
+    }
+    at += prefix_256(all, tmp);   // also ends the counting above
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
         const uint32_t c = cnt[w][threadIdx.x];
@@ -436,14 +471,14 @@ __global__ __launch_bounds__(256) void k_embed_sum(SumArgs a, int64_t row0, int6
             }
 #pragma unroll
             for (int q = 0; q < U; ++q)
-                x[q].load(a.dout, (int64_t)row[q] * a.ld + col);
+                x[q].template load<true>(a.dout, (int64_t)row[q] * a.ld + col);
         } else {
 #pragma unroll
             for (int q = 0; q < U; ++q) {
                 key[q] = none;
                 if (i + q < hi) {
                     key[q] = a.keys[i + q];
-                    x[q].load(a.dout, (int64_t)a.perm[i + q] * a.ld + col);
+                    x[q].template load<true>(a.dout, (int64_t)a.perm[i + q] * a.ld + col);
                 }
             }
         }
@@ -485,16 +520,22 @@ __global__ __launch_bounds__(256) void k_embed_join(SumArgs a, int64_t row0, int
         return;                                     // no run leaves this chunk
     if (a.keys[lo] == key && lo > 0 && a.keys[lo - 1] == key)
         return;                                     // it began in an earlier one
-    // one past the run's last position
-    int64_t l = hi, h = a.n;
-    while (l < h) {
-        const int64_t mid = (l + h) >> 1;
-        if (a.keys[mid] <= key)
-            l = mid + 1;
-        else
-            h = mid;
+    // the run's last chunk: in steps that double, then halving between the
+    // last chunk seen to begin with the id and the first seen not to (a
+    // sorted run: keys[first of q] == key for every chunk up to the last)
+    int64_t last = c + 1, past = last + 1;
+    for (int64_t step = 1; past < a.n_chunks && a.keys[past * a.chunk] == key; step *= 2) {
+        last = past;
+        past = last + step;
     }
-    const int64_t last = (l - 1) / a.chunk;
+    past = past < a.n_chunks ? past : a.n_chunks;
+    while (past - last > 1) {
+        const int64_t mid = (last + past) >> 1;
+        if (a.keys[mid * a.chunk] == key)
+            last = mid;
+        else
+            past = mid;
+    }
     Vec<T, N> s;
     s.load_f32(a.parts + (c * 2 + 1) * a.dim + col);
     int64_t q = c + 1;
@@ -559,14 +600,14 @@ EmbedWork embed_work(int64_t n, int64_t vocab, int64_t dim)
     // chunks long enough that their partial rows are little beside the rows
     // they sum, short enough to fill the GPU
     w.chunk = 16;
-    while (w.chunk < 128 && n * ((dim + 7) / 8) / (w.chunk * 2) >= 131072)
+    while (w.chunk < 128 && n * ((dim + 7) / 8) / (w.chunk * 2) >= 262144)
         w.chunk *= 2;
     w.n_chunks = (n + w.chunk - 1) / w.chunk;
     for (int k = 0; k < 2; ++k) {
         w.keys[k] = take(n * 4);
         w.perm[k] = take(n * 4);
     }
-    w.hist = take(w.n_blocks * 256 * 4);
+    w.hist = take(n ? (w.n_blocks + 1) * 256 * 4 : 0);
     w.parts = take(w.n_chunks * 2 * dim * 4);
     w.bytes = at;
     return w;
@@ -580,17 +621,18 @@ hipError_t launch_lookup(int32_t dtype, const EmbedShape &e, const void *w, int6
     return by_type(dtype, [&](auto t) {
         typedef decltype(t) T;
         constexpr int N = Pack16<T>::N;
-        if (e.dim % N == 0 && ld_w % N == 0 && ld_out % N == 0 && at16(w) && at16(out)) {
-            const int32_t per = (int32_t)(e.dim / N);
-            over_rows(e.n, per, [&](uint32_t nb, int64_t r, int64_t end) {
-                k_lookup<T, N><<<nb, 256, 0, s>>>(e, w, ld_w, out, ld_out, per, r, end);
-            });
-        } else {
-            const int32_t per = (int32_t)e.dim;
-            over_rows(e.n, per, [&](uint32_t nb, int64_t r, int64_t end) {
-                k_lookup<T, 1><<<nb, 256, 0, s>>>(e, w, ld_w, out, ld_out, per, r, end);
-            });
-        }
+        const bool wide = e.dim % N == 0 && ld_w % N == 0 && ld_out % N == 0 && at16(w) && at16(out);
+        const int32_t per = (int32_t)(wide ? e.dim / N : e.dim);
+        // four positions a lane once that still fills the GPU
+        const bool four = wide && e.n * per >= (INT64_C(1) << 20);
+        over_rows(four ? (e.n + 3) / 4 : e.n, per, [&](uint32_t nb, int64_t r, int64_t end) {
+            if (four)
+                k_lookup<T, N, 4><<<nb, 256, 0, s>>>(e, w, ld_w, out, ld_out, per, r, end);
+            else if (wide)
+                k_lookup<T, N, 1><<<nb, 256, 0, s>>>(e, w, ld_w, out, ld_out, per, r, end);
+            else
+                k_lookup<T, 1, 1><<<nb, 256, 0, s>>>(e, w, ld_w, out, ld_out, per, r, end);
+        });
     });
 }
 
@@ -600,7 +642,7 @@ hipError_t launch_embed_grad(int32_t dtype, const EmbedShape &e, const void *dou
     const int64_t elems = e.vocab * e.dim;
     const int64_t clear = accumulate ? 0 : elems;
     // workgroups that clear dW beside a sort kernel's own
-    const uint32_t fill = clear ? (uint32_t)std::min<int64_t>(1024, (clear + 4095) / 4096) : 0;
+    const uint32_t fill = clear ? (uint32_t)std::min<int64_t>(2048, (clear + 4095) / 4096) : 0;
     const EmbedWork w = embed_work(e.n, e.vocab, e.dim);
     char *base = static_cast<char *>(work);
     uint32_t *keys[2], *perm[2];
@@ -614,8 +656,8 @@ hipError_t launch_embed_grad(int32_t dtype, const EmbedShape &e, const void *dou
         ++passes;
     int last = 0;
     if (e.n == 0) {
-        if (fill)   // workgroup 0 has nothing to count
-            k_sort_prefix<<<1 + fill, 1024, 0, s>>>(hist, 0, dw, clear);
+        if (fill)
+            k_sort_count<<<fill, 256, 0, s>>>(e, nullptr, 0, hist, 0, dw, clear);
         return hipGetLastError();
     }
     if (e.n <= kSortSmall) {
@@ -625,8 +667,9 @@ hipError_t launch_embed_grad(int32_t dtype, const EmbedShape &e, const void *dou
         for (int p = 0; p < passes; ++p) {
             const uint32_t *k = p ? keys[last] : nullptr, *i = p ? perm[last] : nullptr;
             const int to = p ? last ^ 1 : 0;
-            k_sort_count<<<nb, 256, 0, s>>>(e, k, 8 * p, hist, w.n_blocks);
-            k_sort_prefix<<<1 + (p ? 0 : fill), 1024, 0, s>>>(hist, w.n_blocks * 256, dw, clear);
+            k_sort_count<<<nb + (p ? 0 : fill), 256, 0, s>>>(e, k, 8 * p, hist, w.n_blocks, dw, clear);
+            if (w.n_blocks > kSortInline)
+                k_sort_prefix<<<1, 1024, 0, s>>>(hist, w.n_blocks);
             k_sort_place<<<nb, 256, 0, s>>>(e, k, i, 8 * p, hist, w.n_blocks, keys[to], perm[to]);
             last = to;
         }

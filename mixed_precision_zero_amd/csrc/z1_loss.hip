@@ -100,17 +100,20 @@ struct Cut {
         tail = (int)(r.vocab - head - nvec * N);
         d_vec = r.d_vec;
     }
+    // LAST: nothing reads these logits again, so the caches need not keep them
+    template <bool LAST>
     __device__ __forceinline__ Pack16<T> load(int64_t v) const
     {
+        const uint4v *at = reinterpret_cast<const uint4v *>(x + head + v * Pack16<T>::N);
         Pack16<T> p;
-        p.raw = *reinterpret_cast<const uint4v *>(x + head + v * Pack16<T>::N);
+        p.raw = LAST ? __builtin_nontemporal_load(at) : *at;
         return p;
     }
     __device__ __forceinline__ void store(int64_t v, const Pack16<T> &p) const
     {
         E *at = d + head + v * Pack16<T>::N;
         if (d_vec)
-            *reinterpret_cast<uint4v *>(at) = p.raw;
+            __builtin_nontemporal_store(p.raw, reinterpret_cast<uint4v *>(at));
         else
 #pragma unroll
             for (int k = 0; k < Pack16<T>::N; ++k)
@@ -158,19 +161,64 @@ __device__ __forceinline__ Stat stream_stat(const Cut<T> &c, float *lds)
         Pack16<T> p[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-            p[q] = c.load(v + q * NT);
+            p[q] = c.template load<false>(v + q * NT);
 #pragma unroll
         for (int q = 0; q < 4; ++q)
             add_vec(a, p[q]);
     }
     for (; v < c.nvec; v += NT)
-        add_vec(a, c.load(v));
+        add_vec(a, c.template load<false>(v));
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
         const int64_t i = c.edge(e);
         if (i >= 0)
             add_one(a, T::up(c.x[i]));
     }
+    return block_stat<NT>(a, lds);
+}
+
+// Statistics of a row, all of whose vectors (NV a lane) and edge elements stay
+// in registers; NV == 0: of a row that is streamed.
+template <typename T, int NT, int NV, bool LAST>
+__device__ __forceinline__ Stat row_stat(const Cut<T> &c, float *lds, Pack16<T> (&v)[NV > 0 ? NV : 1],
+                                         float (&edge)[2])
+{
+    if (NV == 0)
+        return stream_stat<T, NT>(c, lds);
+    constexpr int N = Pack16<T>::N;
+    Stat a{-kInf, 0.f};
+#pragma unroll
+    for (int q = 0; q < NV; ++q) {
+        const int64_t at = threadIdx.x + q * NT;
+        if (at < c.nvec)
+            v[q] = c.template load<false>(at);
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int64_t i = c.edge(e);
+        edge[e] = i >= 0 ? T::up(c.x[i]) : 0.f;
+    }
+#pragma unroll
+    for (int q = 0; q < NV; ++q)
+        if ((int64_t)threadIdx.x + q * NT < c.nvec)
+#pragma unroll
+            for (int e = 0; e < N; ++e)
+                a.m = fmaxf(a.m, T::up(v[q].e[e]));
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+        if (c.edge(e) >= 0)
+            a.m = fmaxf(a.m, edge[e]);
+    const float b = a.base();
+#pragma unroll
+    for (int q = 0; q < NV; ++q)
+        if ((int64_t)threadIdx.x + q * NT < c.nvec)
+#pragma unroll
+            for (int e = 0; e < N; ++e)
+                a.s += fast_exp(T::up(v[q].e[e]) - b);
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+        if (c.edge(e) >= 0)
+            a.s += fast_exp(edge[e] - b);
     return block_stat<NT>(a, lds);
 }
 
@@ -220,13 +268,13 @@ __device__ __forceinline__ void stream_grad(const Cut<T> &c, int64_t y, float d,
         Pack16<T> p[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-            p[q] = c.load(v + q * NT);
+            p[q] = c.template load<true>(v + q * NT);
 #pragma unroll
         for (int q = 0; q < 4; ++q)
             c.store(v + q * NT, grad_vec(p[q], c.head + (v + q * NT) * N, y, d, lse));
     }
     for (; v < c.nvec; v += NT)
-        c.store(v, grad_vec(c.load(v), c.head + v * N, y, d, lse));
+        c.store(v, grad_vec(c.template load<true>(v), c.head + v * N, y, d, lse));
     grad_edges<T, NT>(c, y, d, lse);
 }
 
@@ -245,7 +293,7 @@ __device__ __forceinline__ void zero_row(const Cut<T> &c)
     }
 }
 
-template <typename T, int NT>
+template <typename T, int NT, int NV>
 __global__ __launch_bounds__(NT) void k_logprob(Rows r, int64_t row0, float *logp, float *lse)
 {
     __shared__ float lds[2 * NT / 64];
@@ -260,7 +308,9 @@ __global__ __launch_bounds__(NT) void k_logprob(Rows r, int64_t row0, float *log
         return;
     }
     const Cut<T> c(r, row);
-    const Stat a = stream_stat<T, NT>(c, lds);
+    Pack16<T> v[NV > 0 ? NV : 1];
+    float edge[2];
+    const Stat a = row_stat<T, NT, NV, false>(c, lds, v, edge);
     if (threadIdx.x == 0) {
         const float xy = y < r.vocab ? T::up(c.x[y]) : __builtin_nanf("");
         const float logs = logf(a.s);
@@ -270,11 +320,14 @@ __global__ __launch_bounds__(NT) void k_logprob(Rows r, int64_t row0, float *log
     }
 }
 
+// The last rows first: z1_token_logprob has just read the logits front to
+// back, and the end of them is still in the 256 MB memory-side cache (6144 x
+// 32000 bf16, both kernels and the pairs': 189 us, front to back 208).
 template <typename T, int NT>
 __global__ __launch_bounds__(NT) void k_logprob_grad(Rows r, int64_t row0, const float *lse,
                                                     const float *dlogp)
 {
-    const int64_t row = row0 + blockIdx.x;
+    const int64_t row = row0 + gridDim.x - 1 - blockIdx.x;
     const int64_t y = target_of(r, row);
     const Cut<T> c(r, row);
     if (y < 0) {
@@ -329,52 +382,13 @@ __global__ __launch_bounds__(NT) void k_policy(Rows r, int64_t row0, PolicyPtrs 
         return;
     }
     constexpr int N = Pack16<T>::N;
-    Pack16<T> v[NV > 0 ? NV : 1];
-    float edge[2];
-    Stat a{-kInf, 0.f};
     // read before the barrier below: the gradient may overwrite the logits
     float xy = 0.f;
     if (threadIdx.x == 0)
         xy = y < r.vocab ? T::up(c.x[y]) : __builtin_nanf("");
-    if (NV > 0) {
-#pragma unroll
-        for (int q = 0; q < NV; ++q) {
-            const int64_t at = threadIdx.x + q * NT;
-            if (at < c.nvec)
-                v[q] = c.load(at);
-        }
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int64_t i = c.edge(e);
-            edge[e] = i >= 0 ? T::up(c.x[i]) : 0.f;
-        }
-        float top = -kInf;
-#pragma unroll
-        for (int q = 0; q < NV; ++q)
-            if ((int64_t)threadIdx.x + q * NT < c.nvec)
-#pragma unroll
-                for (int e = 0; e < N; ++e)
-                    top = fmaxf(top, T::up(v[q].e[e]));
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-            if (c.edge(e) >= 0)
-                top = fmaxf(top, edge[e]);
-        a.m = top;
-        const float b = a.base();
-#pragma unroll
-        for (int q = 0; q < NV; ++q)
-            if ((int64_t)threadIdx.x + q * NT < c.nvec)
-#pragma unroll
-                for (int e = 0; e < N; ++e)
-                    a.s += fast_exp(T::up(v[q].e[e]) - b);
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-            if (c.edge(e) >= 0)
-                a.s += fast_exp(edge[e] - b);
-        a = block_stat<NT>(a, lds);
-    } else {
-        a = stream_stat<T, NT>(c, lds);
-    }
+    Pack16<T> v[NV > 0 ? NV : 1];
+    float edge[2];
+    const Stat a = row_stat<T, NT, NV, true>(c, lds, v, edge);
     if (threadIdx.x == 0) {
         const float logs = logf(a.s);
         const float logp = (xy - a.base()) - logs;
@@ -528,7 +542,7 @@ void over_rows(int64_t n, int nt, F &&f)
         f((uint32_t)std::min(step, n - r), r);
 }
 
-// Workgroup size of the streaming kernels, by the row's vectors.
+// Workgroup size of the streaming gradient kernel, by the row's vectors.
 template <typename T, typename F>
 void by_size(int64_t n, int64_t vocab, F &&f)
 {
@@ -541,6 +555,28 @@ void by_size(int64_t n, int64_t vocab, F &&f)
         f(Int<1024>());
 }
 
+// Lanes and vectors a lane (0: streamed) of the kernels that hold a row in
+// registers: the loads of a whole row are then in flight at once.
+template <typename T, typename F>
+void by_row(int64_t vocab, F &&f)
+{
+    const int64_t nv = vocab / Pack16<T>::N;
+    if (nv <= 256)
+        f(Int<64>(), Int<4>());
+    else if (nv <= 1024)
+        f(Int<256>(), Int<4>());
+    else if (nv <= 4096)
+        f(Int<512>(), Int<8>());
+    else if (nv <= 6144)
+        f(Int<512>(), Int<12>());
+    else if (nv <= 8192)
+        f(Int<512>(), Int<16>());
+    else if (nv <= 12288)
+        f(Int<1024>(), Int<12>());
+    else
+        f(Int<1024>(), Int<0>());
+}
+
 }  // namespace
 
 hipError_t launch_logprob(int32_t dtype, const Rows &r, float *logp, float *lse, hipStream_t s)
@@ -549,10 +585,10 @@ hipError_t launch_logprob(int32_t dtype, const Rows &r, float *logp, float *lse,
         return hipSuccess;
     return by_type(dtype, [&](auto t) {
         typedef decltype(t) T;
-        by_size<T>(r.n, r.vocab, [&](auto nt) {
-            constexpr int NT = decltype(nt)::value;
+        by_row<T>(r.vocab, [&](auto nt, auto nvec) {
+            constexpr int NT = decltype(nt)::value, NV = decltype(nvec)::value;
             over_rows(r.n, NT, [&](uint32_t nb, int64_t row0) {
-                k_logprob<T, NT><<<nb, NT, 0, s>>>(r, row0, logp, lse);
+                k_logprob<T, NT, NV><<<nb, NT, 0, s>>>(r, row0, logp, lse);
             });
         });
     });
@@ -581,29 +617,12 @@ hipError_t launch_policy(int32_t dtype, const Rows &r, const PolicyPtrs &p, cons
     if (r.n > 0)
         e = by_type(dtype, [&](auto t) {
             typedef decltype(t) T;
-            const int64_t nv = r.vocab / Pack16<T>::N;
-            const auto go = [&](auto nt, auto nvec) {
+            by_row<T>(r.vocab, [&](auto nt, auto nvec) {
                 constexpr int NT = decltype(nt)::value, NV = decltype(nvec)::value;
                 over_rows(r.n, NT, [&](uint32_t nb, int64_t row0) {
                     k_policy<T, NT, NV><<<nb, NT, 0, s>>>(r, row0, p, k);
                 });
-            };
-            if (!r.d)
-                by_size<T>(r.n, r.vocab, [&](auto nt) { go(nt, Int<0>()); });
-            else if (nv <= 256)
-                go(Int<64>(), Int<4>());
-            else if (nv <= 1024)
-                go(Int<256>(), Int<4>());
-            else if (nv <= 4096)
-                go(Int<512>(), Int<8>());
-            else if (nv <= 6144)
-                go(Int<512>(), Int<12>());
-            else if (nv <= 8192)
-                go(Int<1024>(), Int<8>());
-            else if (nv <= 12288)
-                go(Int<1024>(), Int<12>());
-            else
-                go(Int<1024>(), Int<0>());
+            });
         });
     if (e != hipSuccess)
         return e;

@@ -31,10 +31,7 @@ __device__ __forceinline__ float bf16_to_f32(uint16_t h)
 }
 __device__ __forceinline__ uint16_t f32_to_bf16(float x)
 {
-    const uint32_t u = __float_as_uint(x);
-    if ((u & 0x7fffffffu) > 0x7f800000u)
-        return (uint16_t)((u >> 16) | 0x40u);
-    return (uint16_t)((u + 0x7fffu + ((u >> 16) & 1u)) >> 16);
+    return __builtin_bit_cast(uint16_t, (__bf16)x);
 }
 
 // Element types of the operators' tensors: storage, and conversion from and
@@ -158,7 +155,7 @@ struct EmbedShape {
     float scale;
 };
 
-constexpr int kSortBlock = 2048;   // ids one workgroup of the radix sort handles
+constexpr int kSortBlock = 1024;   // ids one workgroup of the radix sort handles
 constexpr int kSortSmall = 8192;   // ids one workgroup sorts alone
 
 // Where z1_embed_grad's workspace holds what; offsets in bytes.

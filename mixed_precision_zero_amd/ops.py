@@ -13,7 +13,7 @@ from typing import Optional, Sequence
 import numpy as np
 import torch
 
-from .binding import LIB_PATH, _check, _check_tensors, _dptr, _p64, _stream, lib
+from .binding import LIB_PATH, _check, _dptr, _p64, _stream as _any_stream, lib
 
 EXPORTS = ("z1_ops_abi_version", "z1_muon_create", "z1_muon_destroy", "z1_muon_step",
            "z1_muon_orthogonalize", "z1_embed_lookup", "z1_embed_grad_workspace",
@@ -133,13 +133,46 @@ def _rows_of(t, name: str, dtype=None, shape=None) -> int:
 
 
 def _on_gpu(items) -> None:
+    here = torch.cuda.current_device() if torch.cuda.is_initialized() else None
     for t, name in items:
-        if t is None:
+        if t is None or isinstance(t, int):
             continue
-        if t.device.type != "cuda":
+        at = t.get_device()
+        if at < 0:
             raise ValueError(f"{name}: on {t.device}, expected the current GPU")
-        if t.device.index != torch.cuda.current_device():
+        if at != (torch.cuda.current_device() if here is None else here):
             raise ValueError(f"{name}: on {t.device}, expected cuda:{torch.cuda.current_device()}")
+
+
+def _checked(items, rows=()) -> None:
+    """Reject tensors the library would read or write out of bounds or
+    misread, as binding._check_tensors does (items: tensor, name, dtype or
+    None, elements or bytes), with fewer calls into torch: a small operator
+    takes less time than its checks.  rows: further (tensor, name) whose
+    device alone is still to be looked at."""
+    for t, name, dtype, need in items:
+        if t is None or isinstance(t, int):
+            continue
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name}: expected a torch tensor or a device address, "
+                            f"got {type(t).__name__}")
+        if dtype is not None and t.dtype != dtype:
+            raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: not contiguous")
+        have = t.numel() if dtype is not None else t.numel() * t.element_size()
+        if have < need:
+            unit = "elements" if dtype is not None else "bytes"
+            raise ValueError(f"{name}: {have} {unit}, the call touches {need}")
+    _on_gpu([(t, name) for t, name, _, _ in items])
+    _on_gpu(rows)
+
+
+def _stream(stream):
+    """hipStream_t of a torch stream (default: torch's current stream)."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) or None
+    return _any_stream(stream)
 
 
 # --------------------------------------------------------------------------
@@ -193,7 +226,7 @@ def z1_muon_create(shapes: Sequence, grads: Sequence, *, momentum: Optional[Sequ
         raise TypeError(f"grads: dtype {gtype}, expected float32 or bfloat16")
     want = dict(grads=gtype, momentum=torch.float32, master=torch.float32,
                 weights=torch.bfloat16, ortho=torch.bfloat16)
-    _check_tensors([(x[i], f"{name}[{i}]", want[name], int(rows[i] * cols[i]))
+    _checked([(x[i], f"{name}[{i}]", want[name], int(rows[i] * cols[i]))
                     for name, x in lists.items() if x is not None for i in range(n)])
 
     def table(x):
@@ -221,7 +254,7 @@ def z1_muon_step(muon: Muon, *, lr: float, momentum: float = 0.95, weight_decay:
     """One update of every bound matrix.  d_S: device float64, the squared
     global gradient norm, needed when clip > 0."""
     if d_S is not None:
-        _check_tensors([(d_S, "d_S", torch.float64, 1)])
+        _checked([(d_S, "d_S", torch.float64, 1)])
     hp = MuonHP(lr, momentum, weight_decay, clip, int(bool(nesterov)), 0)
     _check(lib.z1_muon_step(muon.handle, ctypes.byref(hp), _dptr(d_S), _stream(stream)),
            "z1_muon_step")
@@ -276,11 +309,10 @@ def z1_embed_grad(ids, dout, dweight, *, scale: float = 1.0, accumulate: bool = 
     vocab, dim = dweight.shape
     args = _embed_args(ids, vocab, dim, dt, scale)
     ld = _rows_of(dout, "dout", None, (ids.numel(), dim))
-    _check_tensors([(dweight, "dweight", torch.float32, vocab * dim),
-                    (workspace, "workspace", None, z1_embed_grad_workspace(ids.numel(), vocab, dim))])
-    _on_gpu([(ids, "ids"), (dout, "dout")])
-    nbytes = workspace.numel() * workspace.element_size() if isinstance(workspace, torch.Tensor) \
-        else z1_embed_grad_workspace(ids.numel(), vocab, dim)
+    need = z1_embed_grad_workspace(ids.numel(), vocab, dim)
+    _checked([(dweight, "dweight", torch.float32, vocab * dim), (workspace, "workspace", None, need)],
+             ((ids, "ids"), (dout, "dout")))
+    nbytes = workspace.numel() * workspace.element_size() if isinstance(workspace, torch.Tensor) else need
     _check(lib.z1_embed_grad(ctypes.byref(args), dout.data_ptr(), ld, dweight.data_ptr(),
                              int(bool(accumulate)), _dptr(workspace), nbytes, _stream(stream)),
            "z1_embed_grad")
@@ -299,16 +331,12 @@ def _logits_args(logits, targets) -> Logits:
     return Logits(logits.shape[0], logits.shape[1], logits.data_ptr(), ld, targets.data_ptr(), it, dt)
 
 
-def _vectors(n: int, items) -> None:
-    _check_tensors([(t, name, torch.float32, n) for t, name in items])
-
-
 def z1_token_logprob(logits, targets, logp, lse=None, *, stream=None) -> None:
     """logp[r] = log softmax(logits[r])[targets[r]] and lse[r], fp32; 0 where
     the target is negative, NaN where it is the vocabulary's size or more."""
     x = _logits_args(logits, targets)
-    _vectors(x.n_rows, [(logp, "logp"), (lse, "lse")])
-    _on_gpu([(logits, "logits"), (targets, "targets")])
+    _checked([(logp, "logp", torch.float32, x.n_rows), (lse, "lse", torch.float32, x.n_rows)],
+             ((logits, "logits"), (targets, "targets")))
     _check(lib.z1_token_logprob(ctypes.byref(x), _dptr(logp), _dptr(lse), _stream(stream)),
            "z1_token_logprob")
 
@@ -318,8 +346,8 @@ def z1_logprob_grad(logits, targets, lse, dlogp, dlogits, *, stream=None) -> Non
     in the logits' type; dlogits may be logits."""
     x = _logits_args(logits, targets)
     ld = _rows_of(dlogits, "dlogits", logits.dtype, logits.shape)
-    _vectors(x.n_rows, [(lse, "lse"), (dlogp, "dlogp")])
-    _on_gpu([(logits, "logits"), (targets, "targets"), (dlogits, "dlogits")])
+    _checked([(lse, "lse", torch.float32, x.n_rows), (dlogp, "dlogp", torch.float32, x.n_rows)],
+             ((logits, "logits"), (targets, "targets"), (dlogits, "dlogits")))
     _check(lib.z1_logprob_grad(ctypes.byref(x), _dptr(lse), _dptr(dlogp), dlogits.data_ptr(), ld,
                                _stream(stream)), "z1_logprob_grad")
 
@@ -338,10 +366,10 @@ def z1_policy_loss(logits, targets, old_logp, advantages, *, loss, token_loss, l
     if dlogits is not None:
         ld = _rows_of(dlogits, "dlogits", logits.dtype, logits.shape)
     f32 = torch.float32
-    _check_tensors([(t, name, f32, n) for t, name in (
+    _checked([(t, name, f32, n) for t, name in (
         (old_logp, "old_logp"), (advantages, "advantages"), (ref_logp, "ref_logp"),
-        (weights, "weights"), (token_loss, "token_loss"), (logp, "logp"))] + [(loss, "loss", f32, 1)])
-    _on_gpu([(logits, "logits"), (targets, "targets"), (dlogits, "dlogits")])
+        (weights, "weights"), (token_loss, "token_loss"), (logp, "logp"))] + [(loss, "loss", f32, 1)],
+        ((logits, "logits"), (targets, "targets"), (dlogits, "dlogits")))
     a = PolicyArgs(_dptr(old_logp), _dptr(ref_logp), _dptr(advantages), _dptr(weights),
                    float(clip_low), float(clip_high), float(kl_coef), float(scale), _dptr(loss),
                    _dptr(token_loss), _dptr(logp), _dptr(dlogits), ld)
@@ -361,7 +389,7 @@ def z1_preference_loss(logp, ref_logp, targets, cu_seqlens, *, beta: float, scal
         raise ValueError(f"cu_seqlens: {cu_seqlens.numel()} entries, expected 2 pairs + 1")
     pairs = (cu_seqlens.numel() - 1) // 2
     f32 = torch.float32
-    _check_tensors([(targets, "targets", targets.dtype, n),
+    _checked([(targets, "targets", targets.dtype, n),
                     (cu_seqlens, "cu_seqlens", cu_seqlens.dtype, 2 * pairs + 1),
                     (logp, "logp", f32, n), (ref_logp, "ref_logp", f32, n), (dlogp, "dlogp", f32, n),
                     (pair_loss, "pair_loss", f32, pairs), (margins, "margins", f32, pairs),

@@ -71,7 +71,7 @@ def check(ids, w, dout, scale, accumulate, V):
 @pytest.mark.parametrize("dtype", DT, ids=str)
 @pytest.mark.parametrize("T,V,d", [(1, 1, 1), (1, 300, 8), (2, 2, 3), (33, 256, 64), (100, 255, 7), (1000, 65536, 100),
                                    (2047, 257, 72), (2049, 49152, 576), (8192, 1000, 24), (8193, 1000, 24),
-                                   (20000, 70000, 40), (30011, 50, 130)])
+                                   (20000, 70000, 40), (30011, 50, 130), (140001, 300, 8), (262144, 70000, 4)])
 def test_sizes(T, V, d, dtype):
     ids, w, dout = make(T, V, d, dtype, seed=T + d)
     check(ids, w, dout, math.sqrt(d), False, V)
