@@ -577,6 +577,275 @@ void iterate(const MuonTables &t, const MuonUpdate &u, int ns_steps, hipStream_t
     }
 }
 
+// D = f(P P^T, P) for a symmetric P P^T with `side` blocks a side, in LDS, the
+// blocks shared out over 8 waves; f gets P's own element where D and P have
+// the same shape.  What a block reads of a step's depth is read before the
+// first of it is multiplied.  32 x 32 blocks for the larger matrices, 16 x 16
+// ones, of which more waves get some, for the smaller.
+template <typename F>
+__device__ __forceinline__ void square16(const _Float16 *P, int sp, int depth, _Float16 *D, int sd,
+                                         int side, int wave, int lane, F &&f)
+{
+    const int l15 = lane & 15, l4 = lane >> 4;
+    for (int bl = wave; bl < side * side; bl += 8) {
+        const int i = bl / side * 16, j = bl % side * 16;
+        const _Float16 *pa = P + (i + l15) * sp + l4 * 8, *pb = P + (j + l15) * sp + l4 * 8;
+        float4v s[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        int k = 0;
+        for (; k + 128 <= depth; k += 128) {
+            half8 a[4], b[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                a[q] = *reinterpret_cast<const half8 *>(pa + k + 32 * q);
+                b[q] = *reinterpret_cast<const half8 *>(pb + k + 32 * q);
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                s[q & 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[q], b[q], s[q & 1], 0, 0, 0);
+        }
+        for (; k < depth; k += 32)
+            s[0] = __builtin_amdgcn_mfma_f32_16x16x32_f16(*reinterpret_cast<const half8 *>(pa + k),
+                                                          *reinterpret_cast<const half8 *>(pb + k), s[0], 0, 0, 0);
+        // column j + l15, rows i + 4 l4 + (0..3): stored as the mirrored place
+        const half4 own = *reinterpret_cast<const half4 *>(P + (j + l15) * sp + i + 4 * l4);
+        half4 h;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            h[e] = (_Float16)f((s[0][e] + s[1][e]) * kUnscale, (float)own[e]);
+        *reinterpret_cast<half4 *>(D + (j + l15) * sd + i + 4 * l4) = h;
+    }
+}
+
+template <typename F>
+__device__ __forceinline__ void square32(const _Float16 *P, int sp, int depth, _Float16 *D, int sd,
+                                         int side, int wave, int lane, F &&f)
+{
+    const int half = lane >> 5, low = lane & 31;
+    for (int bl = wave; bl < side * side; bl += 8) {
+        const int i = bl / side * 32, j = bl % side * 32;
+        const _Float16 *pa = P + (i + low) * sp + half * 8, *pb = P + (j + low) * sp + half * 8;
+        float16v s;
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+            s[e] = 0.f;
+        for (int k = 0; k < depth; k += 32) {
+            half8 a[2], b[2];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                a[q] = *reinterpret_cast<const half8 *>(pa + k + 16 * q);
+                b[q] = *reinterpret_cast<const half8 *>(pb + k + 16 * q);
+            }
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+                s = __builtin_amdgcn_mfma_f32_32x32x16_f16(a[q], b[q], s, 0, 0, 0);
+        }
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const int ii = i + 8 * g + 4 * half;
+            const half4 own = *reinterpret_cast<const half4 *>(P + (j + low) * sp + ii);
+            half4 h;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                h[e] = (_Float16)f(s[4 * g + e] * kUnscale, (float)own[e]);
+            *reinterpret_cast<half4 *>(D + (j + low) * sd + ii) = h;
+        }
+    }
+}
+
+// A small matrix's whole update in one workgroup: nothing but the caller's
+// tensors crosses memory, and the five steps' fifteen products are separated
+// by barriers instead of launches (64 x 256: 12 us against 62 for 18 launches
+// of 2 to 5 us each, most of it their start and their first loads).
+template <bool BF, bool STEP>
+__global__ __launch_bounds__(512) void k_muon_small(const MuonMat *mats, MuonUpdate u, int ns_steps,
+                                                    float ca, float cb, float cc, double eps)
+{
+    __shared__ __align__(16) char lds[kSmallLds];
+    __shared__ double red[8];
+    const MuonMat &t = mats[blockIdx.x];
+    const int mp = t.mp, np = t.np, sx = np + 8, sy = mp + 8, su = np + 4;
+    _Float16 *X = reinterpret_cast<_Float16 *>(lds);   // [mp][sx]
+    _Float16 *Y = X + mp * sx;                         // [np][sy]
+    _Float16 *A = Y + np * sy, *B = A + mp * sy;       // [mp][sy]
+    float *U = reinterpret_cast<float *>(lds);         // [mp][su], before X and Y
+    const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, low = lane & 31;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+
+    const int numel = t.rows * t.cols;
+    if (numel < mp * np) {   // the padding
+        for (int q = tid; q < mp * su; q += 512)
+            U[q] = 0.f;
+        __syncthreads();
+    }
+    const float c = STEP ? clip_factor(u) : 1.0f;
+    double sum = 0.0;
+    const auto put = [&](int row, int col, float grad, float &mom) {
+        float x = c * grad;
+        if (STEP) {
+            mom = fmaf(u.mu, mom, x);
+            x = u.nesterov ? fmaf(u.mu, mom, x) : mom;
+        }
+        U[t.flip ? col * su + row : row * su + col] = x;
+        sum += (double)x * (double)x;
+    };
+    // N elements a load, 8 loads of a lane in flight (the momentum is written
+    // behind them: a load after a store to what may be its place would wait)
+    const auto take = [&](auto width) {
+        constexpr int N = decltype(width)::value, kBatch = 8;
+        for (int at = tid * N; at < numel; at += 512 * N * kBatch) {
+            float g[kBatch][N], m[kBatch][N];
+#pragma unroll
+            for (int q = 0; q < kBatch; ++q) {
+                const int e = at + 512 * N * q;
+                if (e < numel) {
+                    if (N == 4 && !BF)
+                        *reinterpret_cast<float4v *>(g[q]) =
+                            *reinterpret_cast<const float4v *>(static_cast<const float *>(t.grad) + e);
+                    else if (N == 4) {
+                        const uint2v p = *reinterpret_cast<const uint2v *>(static_cast<const uint16_t *>(t.grad) + e);
+                        g[q][0] = __uint_as_float(p.x << 16);
+                        g[q][N / 4] = __uint_as_float(p.x & 0xffff0000u);
+                        g[q][N / 2] = __uint_as_float(p.y << 16);
+                        g[q][N - 1] = __uint_as_float(p.y & 0xffff0000u);
+                    } else
+                        g[q][0] = load_grad<BF>(t, e);
+                    if (STEP) {
+                        if (N == 4)
+                            *reinterpret_cast<float4v *>(m[q]) = *reinterpret_cast<const float4v *>(t.mom + e);
+                        else
+                            m[q][0] = t.mom[e];
+                    }
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < kBatch; ++q) {
+                const int e = at + 512 * N * q;
+                if (e < numel) {
+                    const int row = (int)((uint32_t)e / (uint32_t)t.cols), col = e - row * t.cols;
+#pragma unroll
+                    for (int k = 0; k < N; ++k)
+                        put(row, col + k, g[q][k], m[q][k]);
+                    if (STEP) {
+                        if (N == 4)
+                            *reinterpret_cast<float4v *>(t.mom + e) = *reinterpret_cast<float4v *>(m[q]);
+                        else
+                            t.mom[e] = m[q][0];
+                    }
+                }
+            }
+        }
+    };
+    if (t.vec && t.cols % 4 == 0)
+        take(std::integral_constant<int, 4>());
+    else
+        take(std::integral_constant<int, 1>());
+    sum = block_sum(sum, red);   // its barriers also end the writes of U
+    const double d = sqrt(sum) + eps;
+    const double r = d == 0.0 ? 0.0 : (double)kScale / d;
+
+    // block q of this wave: number wave + 8 q of the (mp / 32) x (np / 32)
+    const int across = np / 32, blocks = (mp / 32) * across;
+    float4v x[4][4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const int bl = wave + 8 * q;
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+            x[q][g] = float4v{0.f, 0.f, 0.f, 0.f};
+        if (bl < blocks) {
+            const int i = bl / across * 32 + 4 * half, j = bl % across * 32 + low;
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    x[q][g][k] = (float)((double)U[(i + 8 * g + k) * su + j] * r);
+        }
+    }
+    __syncthreads();
+
+    for (int step = 0; step < ns_steps; ++step) {
+        // the operand copies of X
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int bl = wave + 8 * q;
+            if (bl < blocks) {
+                const int i = bl / across * 32 + 4 * half, j = bl % across * 32 + low;
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    half4 h;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        h[k] = (_Float16)x[q][g][k];
+                    *reinterpret_cast<half4 *>(Y + j * sy + i + 8 * g) = h;
+                    *reinterpret_cast<half4 *>(X + (i + 8 * g + (lane & 3)) * sx + (j & ~3)) = quad_transpose(h);
+                }
+            }
+        }
+        __syncthreads();
+        // A = X X^T
+        if (mp >= 96)
+            square32(X, sx, np, A, sy, mp / 32, wave, lane,
+                     [&](float v, float) { return v; });
+        else
+            square16(X, sx, np, A, sy, mp / 16, wave, lane, [&](float v, float) { return v; });
+        __syncthreads();
+        // B = b A + c A A
+        if (mp >= 96)
+            square32(A, sy, mp, B, sy, mp / 32, wave, lane,
+                     [&](float v, float s) { return fmaf(cc, v, cb * s); });
+        else
+            square16(A, sy, mp, B, sy, mp / 16, wave, lane,
+                     [&](float v, float s) { return fmaf(cc, v, cb * s); });
+        __syncthreads();
+        // X = a X + B X, the wave's blocks side by side
+        {
+            float16v acc[4];
+            const _Float16 *pa[4], *pb[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int bl = wave + 8 * q;
+                pa[q] = B + (bl / across * 32 + low) * sy + half * 8;
+                pb[q] = Y + (bl % across * 32 + low) * sy + half * 8;
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    acc[q][e] = 0.f;
+            }
+            for (int k = 0; k < mp; k += 32) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (wave + 8 * q < blocks) {
+                        const half8 a0 = *reinterpret_cast<const half8 *>(pa[q] + k);
+                        const half8 b0 = *reinterpret_cast<const half8 *>(pb[q] + k);
+                        const half8 a1 = *reinterpret_cast<const half8 *>(pa[q] + k + 16);
+                        const half8 b1 = *reinterpret_cast<const half8 *>(pb[q] + k + 16);
+                        acc[q] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a0, b0, acc[q], 0, 0, 0);
+                        acc[q] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a1, b1, acc[q], 0, 0, 0);
+                    }
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+                for (int g = 0; g < 4; ++g)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        x[q][g][k] = fmaf(ca, x[q][g][k], acc[q][4 * g + k] * kUnscale);
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const int bl = wave + 8 * q;
+        if (bl < blocks)
+            put_block<STEP ? kStep : kOrtho>(t, u, bl / across * 32, bl % across * 32, x[q]);
+    }
+}
+
+template <bool BF, bool STEP>
+void small(const MuonTables &t, const MuonUpdate &u, int ns_steps, hipStream_t s)
+{
+    k_muon_small<BF, STEP><<<(uint32_t)t.n_small, 512, 0, s>>>(t.mats + t.n, u, ns_steps, t.a, t.b, t.c, t.eps);
+}
+
 template <bool BF, bool STEP>
 void first(const MuonTables &t, const MuonUpdate &u, hipStream_t s)
 {
@@ -589,8 +858,14 @@ void first(const MuonTables &t, const MuonUpdate &u, hipStream_t s)
 
 hipError_t launch_muon(const MuonTables &t, const MuonUpdate &u, int ns_steps, hipStream_t s)
 {
+    if (t.n_small > 0) {
+        if (t.grad_bf16)
+            u.step ? small<true, true>(t, u, ns_steps, s) : small<true, false>(t, u, ns_steps, s);
+        else
+            u.step ? small<false, true>(t, u, ns_steps, s) : small<false, false>(t, u, ns_steps, s);
+    }
     if (t.n == 0)
-        return hipSuccess;
+        return hipGetLastError();
     if (t.grad_bf16)
         u.step ? first<true, true>(t, u, s) : first<true, false>(t, u, s);
     else

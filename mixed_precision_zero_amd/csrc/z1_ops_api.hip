@@ -239,19 +239,36 @@ z1_status muon_create(z1_muon **out, const z1_muon_bind *b, z1_stream stream)
     m->can_ortho = b->ortho != nullptr;
     m->ns_steps = b->ns_steps;
     MuonTables &t = m->t;
-    t.n = n;
     t.grad_bf16 = b->grad_dtype == Z1_BF16;
     t.a = (float)b->a;
     t.b = (float)b->b;
     t.c = (float)b->c;
     t.eps = b->eps;
-    t.tile = pick_tile(n, b->rows, b->cols);
+    // the matrices of the tiled path first, then the small ones
+    std::vector<int32_t> order, few;
+    std::vector<int64_t> rows, cols;
+    for (int32_t i = 0; i < n; ++i) {
+        if (z1::ops::muon_small(pad_to(std::min(b->rows[i], b->cols[i]), 32),
+                                pad_to(std::max(b->rows[i], b->cols[i]), 32))) {
+            few.push_back(i);
+        } else {
+            order.push_back(i);
+            rows.push_back(b->rows[i]);
+            cols.push_back(b->cols[i]);
+        }
+    }
+    t.n = (int32_t)order.size();
+    t.n_small = (int32_t)few.size();
+    order.insert(order.end(), few.begin(), few.end());
+    t.tile = pick_tile(t.n, rows.data(), cols.data());
 
     std::vector<MuonMat> mats((size_t)n);
     std::vector<MuonChunk> chunks;
     std::vector<MuonTile> cast, sym, full;
-    for (int32_t i = 0; i < n; ++i) {
-        MuonMat &q = mats[(size_t)i];
+    for (int32_t at = 0; at < n; ++at) {
+        const int32_t i = order[(size_t)at];
+        const int32_t side = at < t.n ? t.tile : 32;
+        MuonMat &q = mats[(size_t)at];
         q = MuonMat{};
         q.grad = b->grad[i];
         q.rows = (int32_t)b->rows[i];
@@ -259,8 +276,8 @@ z1_status muon_create(z1_muon **out, const z1_muon_bind *b, z1_stream stream)
         q.flip = q.rows > q.cols;
         q.m = q.flip ? q.cols : q.rows;
         q.n = q.flip ? q.rows : q.cols;
-        q.mp = (int32_t)pad_to(q.m, t.tile);
-        q.np = (int32_t)pad_to(q.n, t.tile);
+        q.mp = (int32_t)pad_to(q.m, side);
+        q.np = (int32_t)pad_to(q.n, side);
         q.vec = aligned(q.grad, 16);
         if (m->can_step) {
             q.mom = b->momentum[i];
@@ -273,14 +290,16 @@ z1_status muon_create(z1_muon **out, const z1_muon_bind *b, z1_stream stream)
         q.vec4 = q.cols % 4 == 0 && aligned(q.master, 16) && aligned(q.weight, 8) && aligned(q.ortho, 8);
         q.lr_scale = b->lr_scale ? b->lr_scale[i] : 1.0;
         q.wd_scale = b->wd_scale ? b->wd_scale[i] : 1.0;
+        if (at >= t.n)
+            continue;
         const int64_t numel = (int64_t)q.rows * q.cols;
         q.part0 = (int64_t)chunks.size();
         for (int64_t s = 0; s < numel; s += z1::ops::kMuonChunk)
-            chunks.push_back(MuonChunk{s, i, (int32_t)std::min<int64_t>(z1::ops::kMuonChunk, numel - s)});
+            chunks.push_back(MuonChunk{s, at, (int32_t)std::min<int64_t>(z1::ops::kMuonChunk, numel - s)});
         q.n_part = (int64_t)chunks.size() - q.part0;
-        add_tiles(cast, i, q.mp / z1::ops::kCastTile, q.np / z1::ops::kCastTile, false);
-        add_tiles(sym, i, q.mp / t.tile, q.mp / t.tile, true);
-        add_tiles(full, i, q.mp / t.tile, q.np / t.tile, false);
+        add_tiles(cast, at, q.mp / z1::ops::kCastTile, q.np / z1::ops::kCastTile, false);
+        add_tiles(sym, at, q.mp / t.tile, q.mp / t.tile, true);
+        add_tiles(full, at, q.mp / t.tile, q.np / t.tile, false);
     }
     spread(sym);
     spread(full);
@@ -305,7 +324,8 @@ z1_status muon_create(z1_muon **out, const z1_muon_bind *b, z1_stream stream)
     const size_t o_part = reserve<double>(bytes, chunks.size());
     const size_t o_inv = reserve<double>(bytes, mats.size());
     std::vector<size_t> offs;
-    for (MuonMat &q : mats) {
+    for (int32_t at = 0; at < t.n; ++at) {
+        const MuonMat &q = mats[(size_t)at];
         const size_t mn = (size_t)q.mp * (size_t)q.np, mm = (size_t)q.mp * (size_t)q.mp;
         offs.push_back(reserve<_Float16>(bytes, mn));
         offs.push_back(reserve<_Float16>(bytes, mn));
@@ -320,7 +340,7 @@ z1_status muon_create(z1_muon **out, const z1_muon_bind *b, z1_stream stream)
         return Z1_ENOMEM;
     }
     char *base = static_cast<char *>(m->block);
-    for (size_t i = 0; i < mats.size(); ++i) {
+    for (size_t i = 0; i < (size_t)t.n; ++i) {
         MuonMat &q = mats[i];
         const size_t *o = &offs[6 * i];
         q.X = reinterpret_cast<_Float16 *>(base + o[0]);
@@ -339,10 +359,12 @@ z1_status muon_create(z1_muon **out, const z1_muon_bind *b, z1_stream stream)
     t.inv = reinterpret_cast<double *>(base + o_inv);
     std::vector<char> host(tables);
     memcpy(&host[o_mats], mats.data(), mats.size() * sizeof(MuonMat));
-    memcpy(&host[o_chunks], chunks.data(), chunks.size() * sizeof(MuonChunk));
-    memcpy(&host[o_cast], cast.data(), cast.size() * sizeof(MuonTile));
-    memcpy(&host[o_sym], sym.data(), sym.size() * sizeof(MuonTile));
-    memcpy(&host[o_full], full.data(), full.size() * sizeof(MuonTile));
+    if (t.n > 0) {
+        memcpy(&host[o_chunks], chunks.data(), chunks.size() * sizeof(MuonChunk));
+        memcpy(&host[o_cast], cast.data(), cast.size() * sizeof(MuonTile));
+        memcpy(&host[o_sym], sym.data(), sym.size() * sizeof(MuonTile));
+        memcpy(&host[o_full], full.data(), full.size() * sizeof(MuonTile));
+    }
     const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     // a create call may wait: the staging buffer is this function's own
     if (hipMemcpyAsync(base, host.data(), tables, hipMemcpyHostToDevice, s) != hipSuccess ||
