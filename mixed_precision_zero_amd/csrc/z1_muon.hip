@@ -560,20 +560,31 @@ __global__ __launch_bounds__(64 * WM * WN) void k_muon_gemm(const MuonMat *mats,
     }
 }
 
-template <int T, int WM, int WN, int PANELS, int RING, bool PAIRED>
+template <Mode MODE>
+void product(const MuonTables &t, const MuonUpdate &u, int src, hipStream_t s)
+{
+    const int p = MODE == kGram ? 0 : MODE == kPoly ? 1 : 2;
+    const uint32_t n = (uint32_t)t.n_tiles[p];
+    if (t.tile[p] == 256)
+        k_muon_gemm<256, 2, 4, 1, 4, true, MODE><<<n, 512, 0, s>>>(t.mats, t.tiles[p], src, t.a, t.b, t.c, u);
+    else if (t.tile[p] == 128)
+        k_muon_gemm<128, 2, 2, 1, 3, false, MODE><<<n, 256, 0, s>>>(t.mats, t.tiles[p], src, t.a, t.b, t.c, u);
+    else
+        k_muon_gemm<64, 2, 2, 2, 3, false, MODE><<<n, 256, 0, s>>>(t.mats, t.tiles[p], src, t.a, t.b, t.c, u);
+}
+
 void iterate(const MuonTables &t, const MuonUpdate &u, int ns_steps, hipStream_t s)
 {
-    constexpr int B = 64 * WM * WN;
     for (int k = 0; k < ns_steps; ++k) {
         const int src = k & 1;
-        k_muon_gemm<T, WM, WN, PANELS, RING, PAIRED, kGram><<<(uint32_t)t.n_sym, B, 0, s>>>(t.mats, t.sym, src, t.a, t.b, t.c, u);
-        k_muon_gemm<T, WM, WN, PANELS, RING, PAIRED, kPoly><<<(uint32_t)t.n_sym, B, 0, s>>>(t.mats, t.sym, src, t.a, t.b, t.c, u);
+        product<kGram>(t, u, src, s);
+        product<kPoly>(t, u, src, s);
         if (k + 1 < ns_steps)
-            k_muon_gemm<T, WM, WN, PANELS, RING, PAIRED, kUpdate><<<(uint32_t)t.n_full, B, 0, s>>>(t.mats, t.full, src, t.a, t.b, t.c, u);
+            product<kUpdate>(t, u, src, s);
         else if (u.step)
-            k_muon_gemm<T, WM, WN, PANELS, RING, PAIRED, kStep><<<(uint32_t)t.n_full, B, 0, s>>>(t.mats, t.full, src, t.a, t.b, t.c, u);
+            product<kStep>(t, u, src, s);
         else
-            k_muon_gemm<T, WM, WN, PANELS, RING, PAIRED, kOrtho><<<(uint32_t)t.n_full, B, 0, s>>>(t.mats, t.full, src, t.a, t.b, t.c, u);
+            product<kOrtho>(t, u, src, s);
     }
 }
 
@@ -870,12 +881,7 @@ hipError_t launch_muon(const MuonTables &t, const MuonUpdate &u, int ns_steps, h
         u.step ? first<true, true>(t, u, s) : first<true, false>(t, u, s);
     else
         u.step ? first<false, true>(t, u, s) : first<false, false>(t, u, s);
-    if (t.tile == 256)
-        iterate<256, 2, 4, 1, 4, true>(t, u, ns_steps, s);
-    else if (t.tile == 128)
-        iterate<128, 2, 2, 1, 3, false>(t, u, ns_steps, s);
-    else
-        iterate<64, 2, 2, 2, 3, false>(t, u, ns_steps, s);
+    iterate(t, u, ns_steps, s);
     return hipGetLastError();
 }
 

@@ -131,47 +131,46 @@ bool coefficients_ok(const z1_muon_bind *b)
 
 int64_t pad_to(int64_t x, int64_t q) { return (x + q - 1) / q * q; }
 
-// The tile side the products run with: the one with the smallest estimate of
-// a step's time.  A product of `tiles` tiles of `panels` 32-deep panels takes
-//   fixed + panels * max(alone, ceil(tiles / 256) * shared)   microseconds,
-// `alone` a tile's time per panel when it has a compute unit for itself and
-// `shared` its share of a full one; the constants are fitted to these times
-// of whole calls (us, 64 / 128 / 256 tiles): 1 x 64 x 256 62 / 111 / 252,
-// 8 x 576 x 1536 260 / 319 / 544, 4 x 1024^2 249 / 298 / 523, 1 x 2048^2 388 /
-// 441 / 777, 2 x 2048 x 8192 2403 / 1864 / 2029, 4 x 2048^2 1263 / 1043 /
-// 1023, 24 x 2048^2 7936 / 6364 / 5551, 1 x 4096 x 11008 5946 / 4106 / 3651;
-// the estimate picks the fastest of the three in all of them.
-int pick_tile(int32_t n, const int64_t *rows, const int64_t *cols)
+// The tile side a product runs with (0: X X^T, 1: A A, 2: B X): the one with
+// the smallest estimate of its time,
+//   fixed + panels * (time of a 32-deep panel)   microseconds,
+// where r = ceil(tiles / 256) tiles fall to the busiest compute unit and a
+// panel takes 0.1 r for tiles of 64, max(0.43, 0.36 r - 0.3) for 128 (which
+// overlap two or three to a unit) and 0.68, or 0.88 r from two on, for 256
+// (one to a unit).  Measured (64 / 128 / 256, us): whole calls 2 x 333 x 1537
+// 130 / 238 / 493, 4 x 1024^2 249 / 298 / 523, 1 x 2048^2 388 / 441 / 777,
+// 24 x 2048^2 7936 / 6364 / 5551; single products of 2 x 2048 x 8192
+// (128 / 256) 112 / 157, 34 / 53 and 207 / 181, of 4 x 2048^2 62 / 62, 63 / 65
+// and 113 / 87, of 4096 x 11008 245 / 250, 99 / 104 and 472 / 401.
+int pick_tile(int product, int32_t n, const int64_t *rows, const int64_t *cols)
 {
 #ifdef Z1_MUON_TILE
     return Z1_MUON_TILE;   // for measuring one side against another
 #endif
     static const struct {
         int side;
-        double fixed, alone, shared;
-    } kTiles[3] = {{64, 2.5, 0.16, 0.112}, {128, 6.0, 0.32, 0.327}, {256, 13.0, 0.6, 0.88}};
-    int tile = 0;
+        double fixed;
+    } kTiles[3] = {{64, 3.0}, {128, 6.0}, {256, 13.0}};
+    int tile = 64;
     double best = 0.0;
     for (const auto &c : kTiles) {
-        // gram, polynomial and update product: tiles, tiles * panels, longest
-        double tiles[3] = {}, work[3] = {}, deep[3] = {};
+        double tiles = 0.0, work = 0.0;
         for (int32_t i = 0; i < n; ++i) {
             const double m = (double)pad_to(std::min(rows[i], cols[i]), c.side);
             const double w = (double)pad_to(std::max(rows[i], cols[i]), c.side);
             const double q = m / c.side;
-            const double t[3] = {q * (q + 1) / 2, q * (q + 1) / 2, q * (w / c.side)};
-            const double k[3] = {w / 32, m / 32, m / 32};
-            for (int p = 0; p < 3; ++p) {
-                tiles[p] += t[p];
-                work[p] += t[p] * k[p];
-                deep[p] = std::max(deep[p], k[p]);
-            }
+            const double t = product == 2 ? q * (w / c.side) : q * (q + 1) / 2;
+            tiles += t;
+            work += t * (product == 0 ? w : m) / 32;
         }
-        double cost = 0.0;
-        for (int p = 0; p < 3 && n > 0; ++p)
-            cost += c.fixed + std::max(deep[p] * c.alone,
-                                       ceil(tiles[p] / 256.0) * (work[p] / tiles[p]) * c.shared);
-        if (tile == 0 || cost < best) {
+        if (n == 0)
+            break;
+        const double r = ceil(tiles / 256.0);
+        const double panel = c.side == 64 ? 0.1 * r
+                             : c.side == 128 ? std::max(0.43, 0.36 * r - 0.3)
+                                             : (r > 1.0 ? 0.88 * r : 0.68);
+        const double cost = c.fixed + work / tiles * panel;
+        if (c.side == 64 || cost < best) {
             best = cost;
             tile = c.side;
         }
@@ -260,14 +259,18 @@ z1_status muon_create(z1_muon **out, const z1_muon_bind *b, z1_stream stream)
     t.n = (int32_t)order.size();
     t.n_small = (int32_t)few.size();
     order.insert(order.end(), few.begin(), few.end());
-    t.tile = pick_tile(t.n, rows.data(), cols.data());
+    int32_t whole = 64;   // sides are padded to whole tiles of every product
+    for (int p = 0; p < 3; ++p) {
+        t.tile[p] = pick_tile(p, t.n, rows.data(), cols.data());
+        whole = std::max(whole, t.tile[p]);
+    }
 
     std::vector<MuonMat> mats((size_t)n);
     std::vector<MuonChunk> chunks;
-    std::vector<MuonTile> cast, sym, full;
+    std::vector<MuonTile> cast, tiles[3];
     for (int32_t at = 0; at < n; ++at) {
         const int32_t i = order[(size_t)at];
-        const int32_t side = at < t.n ? t.tile : 32;
+        const int32_t side = at < t.n ? whole : 32;
         MuonMat &q = mats[(size_t)at];
         q = MuonMat{};
         q.grad = b->grad[i];
@@ -298,28 +301,29 @@ z1_status muon_create(z1_muon **out, const z1_muon_bind *b, z1_stream stream)
             chunks.push_back(MuonChunk{s, at, (int32_t)std::min<int64_t>(z1::ops::kMuonChunk, numel - s)});
         q.n_part = (int64_t)chunks.size() - q.part0;
         add_tiles(cast, at, q.mp / z1::ops::kCastTile, q.np / z1::ops::kCastTile, false);
-        add_tiles(sym, at, q.mp / t.tile, q.mp / t.tile, true);
-        add_tiles(full, at, q.mp / t.tile, q.np / t.tile, false);
+        for (int p = 0; p < 3; ++p)
+            add_tiles(tiles[p], at, q.mp / t.tile[p], (p == 2 ? q.np : q.mp) / t.tile[p], p < 2);
     }
-    spread(sym);
-    spread(full);
+    for (auto &list : tiles)
+        spread(list);
     t.n_chunks = (int64_t)chunks.size();
     t.n_cast = (int64_t)cast.size();
-    t.n_sym = (int64_t)sym.size();
-    t.n_full = (int64_t)full.size();
+    for (int p = 0; p < 3; ++p)
+        t.n_tiles[p] = (int64_t)tiles[p].size();
     if (n == 0) {
         *out = m.release();
         return Z1_OK;
     }
-    if (std::max(std::max(t.n_chunks, t.n_cast), std::max(t.n_sym, t.n_full)) > (int64_t)INT32_MAX / 512)
+    if (std::max({t.n_chunks, t.n_cast, t.n_tiles[0], t.n_tiles[1], t.n_tiles[2]}) > (int64_t)INT32_MAX / 512)
         return Z1_EINVAL;   // more workgroups than one launch takes
 
     size_t bytes = 0;
     const size_t o_mats = reserve<MuonMat>(bytes, mats.size());
     const size_t o_chunks = reserve<MuonChunk>(bytes, chunks.size());
     const size_t o_cast = reserve<MuonTile>(bytes, cast.size());
-    const size_t o_sym = reserve<MuonTile>(bytes, sym.size());
-    const size_t o_full = reserve<MuonTile>(bytes, full.size());
+    size_t o_tiles[3];
+    for (int p = 0; p < 3; ++p)
+        o_tiles[p] = reserve<MuonTile>(bytes, tiles[p].size());
     const size_t tables = bytes;
     const size_t o_part = reserve<double>(bytes, chunks.size());
     const size_t o_inv = reserve<double>(bytes, mats.size());
@@ -353,8 +357,8 @@ z1_status muon_create(z1_muon **out, const z1_muon_bind *b, z1_stream stream)
     t.mats = reinterpret_cast<MuonMat *>(base + o_mats);
     t.chunks = reinterpret_cast<MuonChunk *>(base + o_chunks);
     t.cast = reinterpret_cast<MuonTile *>(base + o_cast);
-    t.sym = reinterpret_cast<MuonTile *>(base + o_sym);
-    t.full = reinterpret_cast<MuonTile *>(base + o_full);
+    for (int p = 0; p < 3; ++p)
+        t.tiles[p] = reinterpret_cast<MuonTile *>(base + o_tiles[p]);
     t.partials = reinterpret_cast<double *>(base + o_part);
     t.inv = reinterpret_cast<double *>(base + o_inv);
     std::vector<char> host(tables);
@@ -362,8 +366,8 @@ z1_status muon_create(z1_muon **out, const z1_muon_bind *b, z1_stream stream)
     if (t.n > 0) {
         memcpy(&host[o_chunks], chunks.data(), chunks.size() * sizeof(MuonChunk));
         memcpy(&host[o_cast], cast.data(), cast.size() * sizeof(MuonTile));
-        memcpy(&host[o_sym], sym.data(), sym.size() * sizeof(MuonTile));
-        memcpy(&host[o_full], full.data(), full.size() * sizeof(MuonTile));
+        for (int p = 0; p < 3; ++p)
+            memcpy(&host[o_tiles[p]], tiles[p].data(), tiles[p].size() * sizeof(MuonTile));
     }
     const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     // a create call may wait: the staging buffer is this function's own

@@ -103,14 +103,14 @@ struct MuonTables {
     const MuonMat *mats;
     const MuonChunk *chunks;   // elementwise pass; chunk q writes partial q
     const MuonTile *cast;      // kCastTile square tiles of the padded X
-    const MuonTile *sym;       // GEMM tiles with ti >= tj of the mp x mp products
-    const MuonTile *full;      // GEMM tiles of the mp x np product
-    int64_t n_chunks, n_cast, n_sym, n_full;
+    // the tiles of the products X X^T and A A (ti >= tj) and B X, and their side
+    const MuonTile *tiles[3];
+    int64_t n_chunks, n_cast, n_tiles[3];
+    int32_t tile[3];           // 64, 128 or 256
     double *partials;          // [n_chunks]
     double *inv;               // [n]  1 / (|U|_F + eps)
     int32_t n;                 // matrices of the tiled path: mats[0 .. n - 1]
     int32_t n_small;           // those one workgroup takes whole: the n_small after them
-    int32_t tile;              // GEMM tile side: 64, 128 or 256
     int32_t grad_bf16;
     float a, b, c;
     double eps;
