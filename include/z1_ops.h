@@ -93,8 +93,10 @@ typedef struct z1_muon_hp {
 
 /* Creates the handle on the current GPU: tile tables and the workspace (10
  * bytes per element and 4 per element of the smaller side squared, padded to
- * tiles).  Errors: Z1_EINVAL for null pointers, sizes, an unknown dtype, or
- * coefficients for which p leaves the range the fp16 operands hold (|p| > 3.9
+ * tiles of up to 256; none for matrices that fit one workgroup, up to about 64
+ * x 512 or 128 x 160).  Waits for its upload.  Errors: Z1_EINVAL for null
+ * pointers, sizes (or more than about 1.7e10 elements in all), an unknown
+ * dtype, or coefficients for which p leaves the range the fp16 operands hold (|p| > 3.9
  * or |b s + c s^2| > 3.9 somewhere on the values the iteration can reach;
  * ns_steps included); Z1_EALIGN; Z1_ENOMEM; Z1_EHIP. */
 z1_status z1_muon_create(z1_muon **out, const z1_muon_bind *bind, z1_stream stream);
@@ -161,7 +163,8 @@ typedef struct z1_logits {
 z1_status z1_token_logprob(const z1_logits *x, float *logp, float *lse, z1_stream stream);
 
 /* dlogits_rv = dlogp_r (1[v == y_r] - exp(x_rv - lse_r)), rounded once to
- * dtype, ld_d elements between rows; dlogits may be the logits themselves. */
+ * dtype, ld_d elements between rows; dlogits may be the logits themselves
+ * (with the same row distance, else Z1_EINVAL), but not overlap them otherwise. */
 z1_status z1_logprob_grad(const z1_logits *x, const float *lse, const float *dlogp,
                           void *dlogits, int64_t ld_d, z1_stream stream);
 
@@ -172,7 +175,7 @@ z1_status z1_logprob_grad(const z1_logits *x, const float *lse, const float *dlo
  *   loss = scale * sum_r w_r l_r      dlogits = d loss / d logits
  * token_loss gets l_r (0 where not counted).  ref_logp may be NULL (no KL
  * term), weights NULL (all 1), dlogits NULL (no gradient), logp NULL;
- * dlogits may be the logits themselves.  Where the minimum's two sides are
+ * dlogits may be the logits themselves, as above.  Where the minimum's two sides are
  * equal with rho outside the clamp (A = 0), the gradient is the clamp's. */
 typedef struct z1_policy_args {
     const float *old_logp, *ref_logp, *advantages, *weights; /* fp32 [n_rows] */

@@ -197,7 +197,7 @@ __global__ __launch_bounds__(256) void k_muon_cast(const MuonMat *mats, const Mu
     }
 }
 
-enum Mode { kGram, kPoly, kUpdate, kOrtho, kStep };
+enum Mode { kGram, kGramPart, kPoly, kUpdate, kOrtho, kStep };
 
 // Transposes 4 x 4 halves across 4 lanes: lane q's column becomes row q.
 __device__ __forceinline__ half4 quad_transpose(half4 h)
@@ -332,7 +332,7 @@ template <int T, int WM, int WN, int PANELS, int RING, bool PAIRED, Mode MODE>
 __global__ __launch_bounds__(64 * WM * WN) void k_muon_gemm(const MuonMat *mats,
                                                             const MuonTile *tiles, int src,
                                                             float ca, float cb, float cc,
-                                                            MuonUpdate u)
+                                                            MuonUpdate u, float *parts, int splits)
 {
     constexpr int NW = WM * WN;
     constexpr int TM = T / WM / 32, TN = T / WN / 32;
@@ -351,10 +351,16 @@ __global__ __launch_bounds__(64 * WM * WN) void k_muon_gemm(const MuonMat *mats,
     const _Float16 *P, *Q;
     int64_t p_step, q_step;
     int K;
-    if (MODE == kGram) {
+    if (MODE == kGram || MODE == kGramPart) {
         P = Q = t.X;
         K = t.np;
         p_step = q_step = (int64_t)t.mp * 32;
+        if (MODE == kGramPart) {   // one of `splits` equal pieces of the depth
+            const int piece = (t.np / 64 + splits - 1) / splits * 64;
+            const int first = tl.part % splits * piece;
+            P = Q = t.X + (int64_t)first * t.mp;
+            K = max(0, min(piece, t.np - first));
+        }
     } else if (MODE == kPoly) {
         P = Q = t.A;
         K = t.mp;
@@ -483,6 +489,19 @@ __global__ __launch_bounds__(64 * WM * WN) void k_muon_gemm(const MuonMat *mats,
     // Four lanes' 4 x 4 halves are transposed for the 8 bytes of the other.
     // What a block reads is read before any of it is written: a load behind a
     // store to what may be the same place waits for it (20 us a 256 tile).
+    if (MODE == kGramPart) {
+        float *to = parts + (int64_t)tl.part * T * T + wave * TM * TN * 1024 + lane * 4;
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+#pragma unroll
+                for (int g = 0; g < 4; ++g)
+                    *reinterpret_cast<float4v *>(to + (i * TN + j) * 1024 + g * 256) =
+                        float4v{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2],
+                                acc[i][j][4 * g + 3]};
+        return;
+    }
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
         const int64_t bi = i0 / 32 + wm * TM + i;
@@ -560,24 +579,64 @@ __global__ __launch_bounds__(64 * WM * WN) void k_muon_gemm(const MuonMat *mats,
     }
 }
 
+// A = X X^T from the pieces' sums, added in order: a workgroup of four waves
+// per 64 x 64 tile, lanes as in the product.
+__global__ __launch_bounds__(256) void k_muon_join(const MuonMat *mats, const MuonTile *tiles,
+                                                   const float *parts, int splits)
+{
+    const MuonTile tl = tiles[blockIdx.x];
+    const MuonMat &t = mats[tl.mat];
+    const int lane = threadIdx.x & 63, half = lane >> 5, low = lane & 31;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t bi = tl.ti * 2 + wave / 2, bj = tl.tj * 2 + wave % 2;
+    const float *from = parts + (int64_t)tl.part * splits * 4096 + wave * 1024 + lane * 4;
+    float4v s[4];
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+        s[g] = *reinterpret_cast<const float4v *>(from + g * 256);
+#pragma unroll 4
+    for (int q = 1; q < splits; ++q)
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+            s[g] += *reinterpret_cast<const float4v *>(from + (int64_t)q * 4096 + g * 256);
+    _Float16 *at = t.A + (bi * t.mp + bj * 32 + low) * 32 + half * 4;
+    _Float16 *mirror = t.A + (bj * t.mp + bi * 32 + half * 4 + (lane & 3)) * 32 + (low & ~3);
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+        half4 h;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            h[k] = (_Float16)(s[g][k] * kUnscale);
+        *reinterpret_cast<half4 *>(at + g * 8) = h;
+        if (tl.ti != tl.tj)
+            *reinterpret_cast<half4 *>(mirror + g * 256) = quad_transpose(h);
+    }
+}
+
 template <Mode MODE>
 void product(const MuonTables &t, const MuonUpdate &u, int src, hipStream_t s)
 {
     const int p = MODE == kGram ? 0 : MODE == kPoly ? 1 : 2;
     const uint32_t n = (uint32_t)t.n_tiles[p];
     if (t.tile[p] == 256)
-        k_muon_gemm<256, 2, 4, 1, 4, true, MODE><<<n, 512, 0, s>>>(t.mats, t.tiles[p], src, t.a, t.b, t.c, u);
+        k_muon_gemm<256, 2, 4, 1, 4, true, MODE><<<n, 512, 0, s>>>(t.mats, t.tiles[p], src, t.a, t.b, t.c, u, nullptr, 1);
     else if (t.tile[p] == 128)
-        k_muon_gemm<128, 2, 2, 1, 3, false, MODE><<<n, 256, 0, s>>>(t.mats, t.tiles[p], src, t.a, t.b, t.c, u);
+        k_muon_gemm<128, 2, 2, 1, 3, false, MODE><<<n, 256, 0, s>>>(t.mats, t.tiles[p], src, t.a, t.b, t.c, u, nullptr, 1);
     else
-        k_muon_gemm<64, 2, 2, 2, 3, false, MODE><<<n, 256, 0, s>>>(t.mats, t.tiles[p], src, t.a, t.b, t.c, u);
+        k_muon_gemm<64, 2, 2, 2, 3, false, MODE><<<n, 256, 0, s>>>(t.mats, t.tiles[p], src, t.a, t.b, t.c, u, nullptr, 1);
 }
 
 void iterate(const MuonTables &t, const MuonUpdate &u, int ns_steps, hipStream_t s)
 {
     for (int k = 0; k < ns_steps; ++k) {
         const int src = k & 1;
-        product<kGram>(t, u, src, s);
+        if (t.splits > 1) {
+            k_muon_gemm<64, 2, 2, 2, 3, false, kGramPart><<<(uint32_t)(t.n_tiles[0] * t.splits), 256, 0, s>>>(
+                t.mats, t.pieces, src, t.a, t.b, t.c, u, t.parts, t.splits);
+            k_muon_join<<<(uint32_t)t.n_tiles[0], 256, 0, s>>>(t.mats, t.tiles[0], t.parts, t.splits);
+        } else {
+            product<kGram>(t, u, src, s);
+        }
         product<kPoly>(t, u, src, s);
         if (k + 1 < ns_steps)
             product<kUpdate>(t, u, src, s);

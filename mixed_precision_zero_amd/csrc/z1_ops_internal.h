@@ -90,7 +90,8 @@ struct MuonMat {
 };
 
 struct MuonTile {
-    int32_t mat, ti, tj, pad;
+    int32_t mat, ti, tj;
+    int32_t part;   // X X^T: the tile's number, or splits times it plus the piece's
 };
 
 // A piece of one matrix for the elementwise pass.
@@ -107,6 +108,10 @@ struct MuonTables {
     const MuonTile *tiles[3];
     int64_t n_chunks, n_cast, n_tiles[3];
     int32_t tile[3];           // 64, 128 or 256
+    // X X^T of few tiles and much depth: every tile in `splits` pieces of it
+    const MuonTile *pieces;    // [n_tiles[0] * splits]
+    float *parts;              // [n_tiles[0] * splits][64 * 64]
+    int32_t splits;            // 1: not split
     double *partials;          // [n_chunks]
     double *inv;               // [n]  1 / (|U|_F + eps)
     int32_t n;                 // matrices of the tiled path: mats[0 .. n - 1]

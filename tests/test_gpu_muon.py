@@ -59,7 +59,7 @@ def matrix(shape, seed, spectrum="gauss"):
 
 SHAPES = [[(1, 1)], [(1, 300)], [(300, 1)], [(2, 3)], [(64, 64)], [(65, 129)], [(200, 72)], [(64, 512)], [(33, 1000)], [(96, 288)], [(160, 128)], [(161, 128)], [(1024, 32)],
           [(512, 1000), (64, 64), (1000, 512), (1, 5)], [(127, 128), (128, 127)],
-          [(2304, 700)], [(2048, 2048), (2048, 2048)], [(2100, 5000)]]
+          [(2304, 700)], [(170, 4100)], [(200, 3000), (8000, 70)], [(150, 1600), (64, 64)], [(2048, 2048), (2048, 2048)], [(2100, 5000)]]
 
 
 @pytest.mark.parametrize("spectrum", ["gauss", "lowrank"])

@@ -153,6 +153,14 @@ def test_losses_refuse_logits(over, status):
     assert B.lib.z1_policy_loss(ctypes.byref(x), ctypes.byref(p), None) == status
 
 
+def test_in_place_gradient_needs_the_same_rows():
+    x = logits_args(ld=104)
+    f = 0x30000
+    p = O.PolicyArgs(f, f, f, f, 0.2, 0.2, 0.1, 1.0, f, f, f, 0x10000, 100)
+    assert B.lib.z1_policy_loss(ctypes.byref(x), ctypes.byref(p), None) == B.Z1_EINVAL
+    assert B.lib.z1_logprob_grad(ctypes.byref(x), f, f, 0x10000, 100, None) == B.Z1_EINVAL
+
+
 @pytest.mark.parametrize("over,status", [
     (dict(clip_low=-0.1), B.Z1_EINVAL), (dict(clip_low=1.5), B.Z1_EINVAL), (dict(clip_high=-0.1), B.Z1_EINVAL),
     (dict(clip_high=float("inf")), B.Z1_EINVAL), (dict(kl_coef=float("nan")), B.Z1_EINVAL),
