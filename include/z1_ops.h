@@ -57,7 +57,7 @@ int32_t z1_ops_abi_version(void);
  *   weights = bf16(master), to nearest even
  *
  * The products take fp16 operands (a fixed power of two above their range's
- * top, see z1_muon.hip) with fp32 accumulators; X itself is carried in fp32,
+ * top, see z1_muon.hip) with fp32 accumulators; X itself is carried in 22 bits,
  * so the error of O stays near 1e-3 of its norm for any spectrum of U.
  * A zero U gives a zero O.  A NaN or infinity anywhere in U spreads over O.
  * ------------------------------------------------------------------------ */
@@ -91,7 +91,7 @@ typedef struct z1_muon_hp {
     int32_t reserved;        /* 0                                           */
 } z1_muon_hp;
 
-/* Creates the handle on the current GPU: tile tables and the workspace (10
+/* Creates the handle on the current GPU: tile tables and the workspace (8
  * bytes per element and 4 per element of the smaller side squared, padded to
  * tiles of up to 256; none for matrices that fit one workgroup, up to about 64
  * x 512 or 128 x 160).  Waits for its upload.  Errors: Z1_EINVAL for null

@@ -10,7 +10,9 @@
 // Every product is of the form C_ij = sum_k P_ik Q_jk with both operands
 // contiguous along k: X X^T, A A^T, and B (X^T)^T from a kept transpose Y of
 // X.  The update's epilogue writes X and Y, which costs 2 more bytes per
-// element and lets one kernel feed all three the same way.
+// element and lets one kernel feed all three the same way.  With the
+// remainder a step's epilogue moves 10 bytes an element (14 with an fp32
+// carry), which is what bounds the update of small matrices.
 //
 // Numbers.  The products take fp16 operands and accumulate in fp32 on the
 // matrix cores.  X, A and B are bounded (|X| <= 1.21, |A| <= 1.46,
@@ -18,11 +20,12 @@
 // leave 3.9), so they are stored times kScale = 2^14: nothing overflows, and
 // values down to 2^-28 stay normal numbers, which matters because X starts
 // with elements near 1 / sqrt(m n).  fp16 keeps 11 bits where bf16 keeps 8.
-// X is carried from step to step in fp32 and only its operand copies are
-// rounded: the step multiplies the small singular values by a = 3.44 each
+// X is carried from step to step in 22 bits, as its fp16 operand copy plus an
+// fp16 remainder (fp32 registers in the one-workgroup kernel), and only the
+// products see it rounded to 11: the step multiplies the small singular values by a = 3.44 each
 // time, and with them every rounding of X, so with X itself rounded to fp16 a
 // low-rank U plus 1% noise comes out 4% off (34% with bf16 throughout), and
-// 0.04% with the fp32 carry (simulated in binary64 with these roundings,
+// 0.04% with the carry (simulated in binary64 with these roundings,
 // 1024 x 1024; a gaussian U: 0.13% against 0.12% and 0.9%).
 #include "z1_ops_internal.h"
 
@@ -63,6 +66,12 @@ __device__ __forceinline__ float load_grad(const MuonMat &t, int64_t i)
 {
     return BF ? bf16_to_f32(static_cast<const uint16_t *>(t.grad)[i])
               : static_cast<const float *>(t.grad)[i];
+}
+
+// What fp16 leaves of x, itself in fp16: together 22 bits.
+__device__ __forceinline__ _Float16 low_part(float x)
+{
+    return (_Float16)(x - (float)(_Float16)x);
 }
 
 // Elementwise pass: the momentum update and the partial sums of U's squares
@@ -144,8 +153,8 @@ __global__ __launch_bounds__(256) void k_muon_norm(const MuonMat *mats, const do
     }
 }
 
-// X = U / (|U|_F + eps), as the fp16 operands X and Y = X^T and the fp32
-// carry, one 64 x 64 tile of the padded X per workgroup through LDS.
+// X = U / (|U|_F + eps), as the fp16 operands X and Y = X^T and the
+// remainder, one 64 x 64 tile of the padded X per workgroup through LDS.
 template <bool BF, bool STEP>
 __global__ __launch_bounds__(256) void k_muon_cast(const MuonMat *mats, const MuonTile *tiles,
                                                    const double *inv, MuonUpdate u)
@@ -187,13 +196,13 @@ __global__ __launch_bounds__(256) void k_muon_cast(const MuonMat *mats, const Mu
         *reinterpret_cast<half8 *>(t.Y[0] + panel_at(t.np, j0 + row, i0 + at)) = y;
     }
     for (int q = threadIdx.x; q < 1024; q += 256) {
-        // 4 rows of one column, lanes in the carry's order
+        // 4 rows of one column, lanes in the remainder's order
         const int block = q >> 8, i = (block >> 1) * 32 + ((q >> 6) & 3) * 8 + ((q >> 5) & 1) * 4;
         const int j = (block & 1) * 32 + (q & 31);
-        float4v y;
+        half4 y;
         for (int k = 0; k < 4; ++k)
-            y[k] = lds[i + k][j];
-        *reinterpret_cast<float4v *>(t.C + carry_at(t.np, i0 + i, j0 + j)) = y;
+            y[k] = low_part(lds[i + k][j]);
+        *reinterpret_cast<half4 *>(t.L + carry_at(t.np, i0 + i, j0 + j)) = y;
     }
 }
 
@@ -538,36 +547,44 @@ __global__ __launch_bounds__(64 * WM * WN) void k_muon_gemm(const MuonMat *mats,
                 }
             }
         } else {
-            float4v x[TN][4];
+            // X is its operand copy (which this tile has just multiplied) plus
+            // the low part
+            half4 hi[TN][4], lo[TN][4];
 #pragma unroll
             for (int j = 0; j < TN; ++j)
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
                     const int64_t bj = j0 / 32 + wn * TN + j;
-                    x[j][g] = *reinterpret_cast<const float4v *>(
-                        t.C + (bi * (t.np >> 5) + bj) * 1024 + lane * 4 + g * 256);
+                    hi[j][g] = *reinterpret_cast<const half4 *>(
+                        t.Y[src] + (bi * t.np + bj * 32 + low) * 32 + half * 4 + g * 8);
+                    lo[j][g] = *reinterpret_cast<const half4 *>(
+                        t.L + (bi * (t.np >> 5) + bj) * 1024 + lane * 4 + g * 256);
                 }
+            float4v x[TN][4];
 #pragma unroll
             for (int j = 0; j < TN; ++j)
 #pragma unroll
                 for (int g = 0; g < 4; ++g)
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        x[j][g][k] = fmaf(ca, x[j][g][k], acc[i][j][4 * g + k] * kUnscale);
+                        x[j][g][k] = fmaf(ca, (float)hi[j][g][k] + (float)lo[j][g][k],
+                                          acc[i][j][4 * g + k] * kUnscale);
 #pragma unroll
             for (int j = 0; j < TN; ++j) {
                 const int64_t bj = j0 / 32 + wn * TN + j;
                 if (MODE == kUpdate) {
-                    float *carry = t.C + (bi * (t.np >> 5) + bj) * 1024 + lane * 4;
+                    _Float16 *rest = t.L + (bi * (t.np >> 5) + bj) * 1024 + lane * 4;
                     _Float16 *yt = t.Y[src ^ 1] + (bi * t.np + bj * 32 + low) * 32 + half * 4;
                     _Float16 *xt = t.X + (bj * t.mp + bi * 32 + half * 4 + (lane & 3)) * 32 + (low & ~3);
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
-                        half4 h;
+                        half4 h, l;
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
+                        for (int k = 0; k < 4; ++k) {
                             h[k] = (_Float16)x[j][g][k];
-                        *reinterpret_cast<float4v *>(carry + g * 256) = x[j][g];
+                            l[k] = low_part(x[j][g][k]);
+                        }
+                        *reinterpret_cast<half4 *>(rest + g * 256) = l;
                         *reinterpret_cast<half4 *>(yt + g * 8) = h;
                         *reinterpret_cast<half4 *>(xt + g * 256) = quad_transpose(h);
                     }

@@ -363,7 +363,7 @@ z1_status muon_create(z1_muon **out, const z1_muon_bind *b, z1_stream stream)
         offs.push_back(reserve<_Float16>(bytes, mn));
         offs.push_back(reserve<_Float16>(bytes, mn));
         offs.push_back(reserve<_Float16>(bytes, mn));
-        offs.push_back(reserve<float>(bytes, mn));
+        offs.push_back(reserve<_Float16>(bytes, mn));
         offs.push_back(reserve<_Float16>(bytes, mm));
         offs.push_back(reserve<_Float16>(bytes, mm));
     }
@@ -379,7 +379,7 @@ z1_status muon_create(z1_muon **out, const z1_muon_bind *b, z1_stream stream)
         q.X = reinterpret_cast<_Float16 *>(base + o[0]);
         q.Y[0] = reinterpret_cast<_Float16 *>(base + o[1]);
         q.Y[1] = reinterpret_cast<_Float16 *>(base + o[2]);
-        q.C = reinterpret_cast<float *>(base + o[3]);
+        q.L = reinterpret_cast<_Float16 *>(base + o[3]);
         q.A = reinterpret_cast<_Float16 *>(base + o[4]);
         q.B = reinterpret_cast<_Float16 *>(base + o[5]);
     }

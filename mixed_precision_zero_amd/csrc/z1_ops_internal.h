@@ -85,7 +85,7 @@ struct MuonMat {
     _Float16 *X;            // mp rows, np deep: the operand copy of X
     _Float16 *Y[2];         // np rows, mp deep: of X^T, one being read and one written
     _Float16 *A, *B;        // mp rows, mp deep
-    float *C;               // the carried X in fp32 (see carry_at)
+    _Float16 *L;            // what the operand copy of X leaves of it (see carry_at)
     double lr_scale, wd_scale;
 };
 
@@ -137,8 +137,8 @@ __host__ __device__ __forceinline__ int64_t panel_at(int64_t rows, int64_t row, 
     return ((k >> 5) * rows + row) * 32 + (k & 31);
 }
 
-// Element (i, j) of the fp32 carry of X (np columns): blocks of 32 x 32 in the
-// order in which the matrix instruction's lanes hold them, 16 bytes a lane.
+// Element (i, j) of X's remainder (np columns): blocks of 32 x 32 in the order
+// in which the matrix instruction's lanes hold them, 4 elements a lane.
 __host__ __device__ __forceinline__ int64_t carry_at(int64_t np, int64_t i, int64_t j)
 {
     const int64_t block = (i >> 5) * (np >> 5) + (j >> 5);
