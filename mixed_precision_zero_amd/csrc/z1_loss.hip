@@ -4,14 +4,18 @@
 // For a row x and target y, lse = log sum_v exp x_v and logp = x_y - lse;
 // d logp / d x_v = 1[v == y] - exp(x_v - lse).  All of it is bound by the
 // bytes of the logits, so each kernel reads a row once, 16 bytes a lane:
-//   - z1_token_logprob keeps a running maximum m and a running sum of
-//     exp(x - m) per lane, rescaled when m grows, and joins the lanes' pairs
-//     in a fixed order;
-//   - z1_policy_loss's gradient needs nothing but the row itself, so the
-//     workgroup keeps the row in registers between the sum and the gradient
-//     and the logits cross memory once in and once out (a vocabulary too long
-//     for that is read twice, the second time mostly from cache);
-//   - z1_logprob_grad is one pass from logits to gradient.
+//   - z1_token_logprob and z1_policy_loss load a whole row into registers, so
+//     all of its loads are in flight at once; each lane takes the maximum m
+//     and the sum of exp(x - m) of what it holds, and the lanes' pairs are
+//     joined in a fixed order (6144 x 32000 bf16: 59 us, 6.6 TB/s; streamed
+//     four vectors at a time, 100).  A row too long for that is streamed with
+//     a running maximum and a sum rescaled when it grows;
+//   - z1_policy_loss's gradient needs nothing but the row itself, so it is
+//     taken from the registers, and the logits cross memory once in and once
+//     out, past the caches (4096 x 49152 bf16: 142 us, 5.7 TB/s both ways;
+//     157 with ordinary stores, 173 with 1024 lanes a row, 152 with 256);
+//   - z1_logprob_grad is one pass from logits to gradient (6144 x 32000 bf16:
+//     114 us, 6.9 TB/s, part of it from cache).
 // Maxima, sums, log-probabilities and losses are fp32 or wider; the gradient
 // is rounded once, to the logits' type.
 #include "z1_ops_internal.h"
