@@ -138,32 +138,40 @@ __global__ __launch_bounds__(256) void k_muon_momentum(const MuonMat *mats,
         partials[blockIdx.x] = s;
 }
 
+// 1 / (|U|_F + eps) from a matrix's partial sums, in a fixed order; called by a
+// workgroup of 256.
+__device__ __forceinline__ double inverse_norm(const MuonMat &t, const double *partials, double eps,
+                                               double *lds)
+{
+    double s = 0.0;
+    for (int64_t q = threadIdx.x; q < t.n_part; q += 256)
+        s += partials[t.part0 + q];
+    const double d = sqrt(block_sum(s, lds)) + eps;
+    return d == 0.0 ? 0.0 : 1.0 / d;
+}
+
 __global__ __launch_bounds__(256) void k_muon_norm(const MuonMat *mats, const double *partials,
                                                    double *inv, double eps)
 {
     __shared__ double lds[4];
-    const MuonMat &t = mats[blockIdx.x];
-    double s = 0.0;
-    for (int64_t q = threadIdx.x; q < t.n_part; q += 256)
-        s += partials[t.part0 + q];
-    s = block_sum(s, lds);
-    if (threadIdx.x == 0) {
-        const double d = sqrt(s) + eps;
-        inv[blockIdx.x] = d == 0.0 ? 0.0 : 1.0 / d;
-    }
+    const double r = inverse_norm(mats[blockIdx.x], partials, eps, lds);
+    if (threadIdx.x == 0)
+        inv[blockIdx.x] = r;
 }
 
 // X = U / (|U|_F + eps), as the fp16 operands X and Y = X^T and the
 // remainder, one 64 x 64 tile of the padded X per workgroup through LDS.
 template <bool BF, bool STEP>
 __global__ __launch_bounds__(256) void k_muon_cast(const MuonMat *mats, const MuonTile *tiles,
-                                                   const double *inv, MuonUpdate u)
+                                                   const double *inv, const double *partials,
+                                                   double eps, MuonUpdate u)
 {
     __shared__ float lds[kCastTile][kCastTile + 1];   // [X row][X column]
+    __shared__ double red[4];
     const MuonTile tl = tiles[blockIdx.x];
     const MuonMat &t = mats[tl.mat];
     const float c = STEP ? clip_factor(u) : 1.0f;
-    const double r = inv[tl.mat] * (double)kScale;
+    const double r = (inv ? inv[tl.mat] : inverse_norm(t, partials, eps, red)) * (double)kScale;
     const int i0 = tl.ti * kCastTile, j0 = tl.tj * kCastTile;
     const int r0 = t.flip ? j0 : i0, c0 = t.flip ? i0 : j0;
     const int cc = threadIdx.x & 63;
@@ -938,8 +946,13 @@ template <bool BF, bool STEP>
 void first(const MuonTables &t, const MuonUpdate &u, hipStream_t s)
 {
     k_muon_momentum<BF, STEP><<<(uint32_t)t.n_chunks, 256, 0, s>>>(t.mats, t.chunks, t.partials, u);
-    k_muon_norm<<<(uint32_t)t.n, 256, 0, s>>>(t.mats, t.partials, t.inv, t.eps);
-    k_muon_cast<BF, STEP><<<(uint32_t)t.n_cast, 256, 0, s>>>(t.mats, t.cast, t.inv, u);
+    // one partial a lane: every tile of the cast adds them by itself, and a
+    // launch is saved (8 x 576 x 1536: 239 -> 236 us, 200 x 300: 71.5 -> 70)
+    const bool apart = t.n_part_most > 256;
+    if (apart)
+        k_muon_norm<<<(uint32_t)t.n, 256, 0, s>>>(t.mats, t.partials, t.inv, t.eps);
+    k_muon_cast<BF, STEP><<<(uint32_t)t.n_cast, 256, 0, s>>>(
+        t.mats, t.cast, apart ? t.inv : nullptr, t.partials, t.eps, u);
 }
 
 }  // namespace

@@ -311,6 +311,7 @@ z1_status muon_create(z1_muon **out, const z1_muon_bind *b, z1_stream stream)
         for (int64_t s = 0; s < numel; s += z1::ops::kMuonChunk)
             chunks.push_back(MuonChunk{s, at, (int32_t)std::min<int64_t>(z1::ops::kMuonChunk, numel - s)});
         q.n_part = (int64_t)chunks.size() - q.part0;
+        t.n_part_most = std::max(t.n_part_most, q.n_part);
         add_tiles(cast, at, q.mp / z1::ops::kCastTile, q.np / z1::ops::kCastTile, false);
         for (int p = 0; p < 3; ++p)
             add_tiles(tiles[p], at, q.mp / t.tile[p], (p == 2 ? q.np : q.mp) / t.tile[p], p < 2);

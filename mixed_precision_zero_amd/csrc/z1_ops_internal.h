@@ -112,6 +112,7 @@ struct MuonTables {
     const MuonTile *pieces;    // [n_tiles[0] * splits]
     float *parts;              // [n_tiles[0] * splits][64 * 64]
     int32_t splits;            // 1: not split
+    int64_t n_part_most;       // partials of the matrix that has most
     double *partials;          // [n_chunks]
     double *inv;               // [n]  1 / (|U|_F + eps)
     int32_t n;                 // matrices of the tiled path: mats[0 .. n - 1]

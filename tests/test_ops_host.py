@@ -26,6 +26,28 @@ def test_every_declared_symbol_is_exported():
     assert O.z1_ops_abi_version() == 1
 
 
+def test_header_is_plain_c(tmp_path):
+    import subprocess
+    src = tmp_path / "t.c"
+    src.write_text('#include "z1_ops.h"\nint main(void) { z1_policy_args a; z1_muon_bind b; (void)a; (void)b; '
+                   'return Z1_OPS_ABI_VERSION - 1; }\n')
+    subprocess.run(["gcc", "-std=c11", "-Wall", "-Werror", "-I", os.path.join(ROOT, "include"), "-c", str(src),
+                    "-o", str(tmp_path / "t.o")], check=True)
+
+
+def test_structures_match_the_header(tmp_path):
+    """Sizes of the ctypes structures against the C compiler's."""
+    import subprocess
+    names = {"z1_muon_bind": O.MuonBind, "z1_muon_hp": O.MuonHP, "z1_embed_args": O.EmbedArgs, "z1_logits": O.Logits,
+             "z1_policy_args": O.PolicyArgs, "z1_preference_args": O.PreferenceArgs}
+    src, exe = tmp_path / "s.c", tmp_path / "s"
+    src.write_text('#include <stdio.h>\n#include "z1_ops.h"\nint main(void) { printf("' + "%d " * len(names) + '", '
+                   + ", ".join(f"(int)sizeof({n})" for n in names) + "); return 0; }\n")
+    subprocess.run(["gcc", "-I", os.path.join(ROOT, "include"), str(src), "-o", str(exe)], check=True)
+    got = subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.split()
+    assert [int(x) for x in got] == [ctypes.sizeof(s) for s in names.values()]
+
+
 def muon_bind(**over):
     rows, cols = (ctypes.c_int64 * 2)(64, 3), (ctypes.c_int64 * 2)(32, 5)
     ptr = lambda base: (ctypes.c_void_p * 2)(base, base + 0x1000)  # noqa: E731
