@@ -121,35 +121,42 @@ def _rows_of(t, name: str, dtype=None, shape=None) -> int:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
     if t.dim() != 2:
         raise ValueError(f"{name}: {t.dim()} dimensions, expected 2")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     n, d = t.shape
-    if d > 1 and t.stride(1) != 1:
+    if t.is_contiguous():
+        return d
+    step = t.stride()
+    if d > 1 and step[1] != 1:
         raise ValueError(f"{name}: rows not contiguous")
-    ld = t.stride(0) if n > 1 else d
+    ld = step[0] if n > 1 else d
     if ld < d:
         raise ValueError(f"{name}: rows overlap (stride {ld} of {d} elements)")
     return ld
 
 
 def _on_gpu(items) -> None:
-    here = torch.cuda.current_device() if torch.cuda.is_initialized() else None
+    """Every tensor on the current GPU.  (A tensor on a GPU means that torch
+    has initialised it, so the current one is asked for without torch's own
+    check of that: a small operator takes less time than its checks.)"""
+    here = -1
     for t, name in items:
         if t is None or isinstance(t, int):
             continue
         at = t.get_device()
         if at < 0:
             raise ValueError(f"{name}: on {t.device}, expected the current GPU")
-        if at != (torch.cuda.current_device() if here is None else here):
-            raise ValueError(f"{name}: on {t.device}, expected cuda:{torch.cuda.current_device()}")
+        if here < 0:
+            here = torch._C._cuda_getDevice()
+        if at != here:
+            raise ValueError(f"{name}: on {t.device}, expected cuda:{here}")
 
 
 def _checked(items, rows=()) -> None:
     """Reject tensors the library would read or write out of bounds or
     misread, as binding._check_tensors does (items: tensor, name, dtype or
-    None, elements or bytes), with fewer calls into torch: a small operator
-    takes less time than its checks.  rows: further (tensor, name) whose
-    device alone is still to be looked at."""
+    None, elements or bytes), with fewer calls into torch.  rows: further
+    (tensor, name) whose device alone is still to be looked at."""
     for t, name, dtype, need in items:
         if t is None or isinstance(t, int):
             continue
@@ -164,14 +171,13 @@ def _checked(items, rows=()) -> None:
         if have < need:
             unit = "elements" if dtype is not None else "bytes"
             raise ValueError(f"{name}: {have} {unit}, the call touches {need}")
-    _on_gpu([(t, name) for t, name, _, _ in items])
-    _on_gpu(rows)
+    _on_gpu([i[:2] for i in items] + list(rows))
 
 
 def _stream(stream):
     """hipStream_t of a torch stream (default: torch's current stream)."""
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) or None
+    if stream is None and torch.cuda.is_initialized():
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()) or None
     return _any_stream(stream)
 
 
@@ -326,7 +332,7 @@ def _logits_args(logits, targets) -> Logits:
     dt = _dtype_of(logits, "logits")
     ld = _rows_of(logits, "logits")
     it = _itype_of(targets, "targets")
-    if tuple(targets.shape) != (logits.shape[0],) or not targets.is_contiguous():
+    if targets.shape != logits.shape[:1] or not targets.is_contiguous():
         raise ValueError(f"targets: expected {logits.shape[0]} contiguous entries")
     return Logits(logits.shape[0], logits.shape[1], logits.data_ptr(), ld, targets.data_ptr(), it, dt)
 
