@@ -675,8 +675,9 @@ void iterate(const MuonTables &t, const MuonUpdate &u, int ns_steps, hipStream_t
 // D = f(P P^T, P) for a symmetric P P^T with `side` blocks a side, in LDS, the
 // blocks shared out over 8 waves; f gets P's own element where D and P have
 // the same shape.  What a block reads of a step's depth is read before the
-// first of it is multiplied.  32 x 32 blocks for the larger matrices, 16 x 16
-// ones, of which more waves get some, for the smaller.
+// first of it is multiplied.  32 x 32 blocks read LDS half as often and are used
+// from 64 a side (64 x 512: 33 us against 39 with 16 x 16 blocks); 16 x 16 ones
+// give four waves work where the side is 32.
 template <typename F>
 __device__ __forceinline__ void square16(const _Float16 *P, int sp, int depth, _Float16 *D, int sd,
                                          int side, int wave, int lane, F &&f)
@@ -749,9 +750,9 @@ __device__ __forceinline__ void square32(const _Float16 *P, int sp, int depth, _
 
 // A small matrix's whole update in one workgroup: nothing but the caller's
 // tensors crosses memory, and the five steps' fifteen products are separated
-// by barriers instead of launches (2 of 64 x 256: 30 us against 62 for 18
+// by barriers instead of launches (2 of 64 x 256: 27 us against 62 for 18
 // launches of 2 to 5 us each; 128 x 160: 33 against 60; 2000 of them: 278
-// against 1242).  What is left is latency: 3.4 us a step of 64 x 256.
+// against 1242).  What is left is latency: 2.8 us a step of 64 x 256.
 template <bool BF, bool STEP>
 __global__ __launch_bounds__(512) void k_muon_small(const MuonMat *mats, MuonUpdate u, int ns_steps,
                                                     float ca, float cb, float cc, double eps)
@@ -879,14 +880,14 @@ __global__ __launch_bounds__(512) void k_muon_small(const MuonMat *mats, MuonUpd
         }
         __syncthreads();
         // A = X X^T
-        if (mp >= 96)
+        if (mp >= 64)
             square32(X, sx, np, A, sy, mp / 32, wave, lane,
                      [&](float v, float) { return v; });
         else
             square16(X, sx, np, A, sy, mp / 16, wave, lane, [&](float v, float) { return v; });
         __syncthreads();
         // B = b A + c A A
-        if (mp >= 96)
+        if (mp >= 64)
             square32(A, sy, mp, B, sy, mp / 32, wave, lane,
                      [&](float v, float s) { return fmaf(cc, v, cb * s); });
         else
