@@ -249,9 +249,9 @@ __device__ __forceinline__ void wait_copies()
 
 // The caller's outputs of one 32 x 32 block of the last X, held as the matrix
 // instruction leaves it: column `low`, rows 8 g + 4 half + k.  Element (i, j)
-// of X sits at i * si + j * sj of the caller's matrix.  A whole block of
-// 16-byte aligned rows is written 8 or 16 bytes a lane without a test per
-// element (4 x 2048 x 2048: 274 us for this product with the tests, 86 for
+// of X sits at i * si + j * sj of the caller's matrix.  A whole block is written
+// without a test per element, 8 or 16 bytes a lane where its rows are 16-byte
+// aligned (4 x 2048 x 2048: 274 us for this product with the tests, 86 for
 // one that writes no outputs).
 template <Mode MODE>
 __device__ __forceinline__ void put_block(const MuonMat &t, const MuonUpdate &u, int64_t i0, int64_t j0,
@@ -264,7 +264,7 @@ __device__ __forceinline__ void put_block(const MuonMat &t, const MuonUpdate &u,
         return MODE == kOrtho ? o : (float)((double)old * decay - step * (double)o);
     };
     const int64_t ii = i0 + half * 4, jj = j0 + low;
-    if (t.vec4 && i0 + 32 <= t.m && j0 + 32 <= t.n) {
+    if (i0 + 32 <= t.m && j0 + 32 <= t.n && (t.vec4 || !t.flip)) {
         float4v w[4];
         if (t.flip) {
             const int64_t at = jj * t.cols + ii;
@@ -286,7 +286,7 @@ __device__ __forceinline__ void put_block(const MuonMat &t, const MuonUpdate &u,
             }
         } else {
             float *m = t.master + ii * t.cols + jj;
-            uint16_t *o = out + (ii + (lane & 3)) * t.cols + (jj & ~3);
+            uint16_t *o = out + (ii + (t.vec4 ? lane & 3 : 0)) * t.cols + (t.vec4 ? jj & ~3 : jj);
             if (MODE == kStep)
 #pragma unroll
                 for (int g = 0; g < 4; ++g)
@@ -303,7 +303,12 @@ __device__ __forceinline__ void put_block(const MuonMat &t, const MuonUpdate &u,
                     if (MODE == kStep)
                         m[(int64_t)(8 * g + k) * t.cols] = w[g][k];
                 }
-                *reinterpret_cast<half4 *>(o + (int64_t)(8 * g) * t.cols) = quad_transpose(h);
+                if (t.vec4)
+                    *reinterpret_cast<half4 *>(o + (int64_t)(8 * g) * t.cols) = quad_transpose(h);
+                else
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        o[(int64_t)(8 * g + k) * t.cols] = __builtin_bit_cast(uint16_t, h[k]);
             }
         }
         return;
