@@ -308,7 +308,7 @@ __device__ __forceinline__ void put_block(const MuonMat &t, const MuonUpdate &u,
                 else
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        o[(int64_t)(8 * g + k) * t.cols] = __builtin_bit_cast(uint16_t, h[k]);
+                        o[(int64_t)(8 * g + k) * t.cols] = f32_to_bf16(w[g][k]);
             }
         }
         return;
