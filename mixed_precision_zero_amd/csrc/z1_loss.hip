@@ -439,16 +439,17 @@ __global__ __launch_bounds__(NT) void k_policy(Rows r, int64_t row0, PolicyPtrs 
 }
 
 // scale * sum_r w_r l_r in binary64, in a fixed order: one workgroup, for it
-// reads 4 or 8 bytes for each row of logits.  A row of weight 0 is not counted
-// (its l is 0 already).
-__global__ __launch_bounds__(1024) void k_loss_sum(const float *l, const float *w, int64_t n,
+// reads 4 to 16 bytes for each row of logits.  A row that does not count (l is
+// 0 there) is left out whatever its weight: 0 times an infinity or a NaN would
+// be the whole loss.
+__global__ __launch_bounds__(1024) void k_loss_sum(const float *l, const float *w, Rows r,
                                                    double scale, float *loss)
 {
     __shared__ double lds[16];
     double s = 0.0;
-    for (int64_t i = threadIdx.x; i < n; i += 1024) {
+    for (int64_t i = threadIdx.x; i < r.n; i += 1024) {
         const float wi = w ? w[i] : 1.f;
-        if (wi != 0.f)
+        if (wi != 0.f && !(w && target_of(r, i) < 0))
             s += (double)l[i] * (double)wi;
     }
     for (int o = 32; o > 0; o >>= 1)
@@ -635,14 +636,16 @@ hipError_t launch_policy(int32_t dtype, const Rows &r, const PolicyPtrs &p, cons
         });
     if (e != hipSuccess)
         return e;
-    k_loss_sum<<<1, 1024, 0, s>>>(p.token_loss, p.w, r.n, scale, loss);
+    k_loss_sum<<<1, 1024, 0, s>>>(p.token_loss, p.w, r, scale, loss);
     return hipGetLastError();
 }
 
 hipError_t launch_preference(const z1_preference_args &a, hipStream_t s)
 {
     k_preference<<<(uint32_t)(a.n_pairs + 1), 256, 0, s>>>(a);
-    k_loss_sum<<<1, 1024, 0, s>>>(a.pair_loss, nullptr, a.n_pairs, a.scale, a.loss);
+    Rows pairs{};
+    pairs.n = a.n_pairs;
+    k_loss_sum<<<1, 1024, 0, s>>>(a.pair_loss, nullptr, pairs, a.scale, a.loss);
     return hipGetLastError();
 }
 

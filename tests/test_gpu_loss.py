@@ -337,3 +337,25 @@ def test_other_stream_and_graph():
         assert same(), k
         call()
         assert same(), k
+
+
+@pytest.mark.parametrize("itype", [torch.int64, torch.int32])
+@pytest.mark.parametrize("weight", [math.inf, -math.inf, math.nan])
+@pytest.mark.parametrize("n", [8, 1500])
+def test_weights_of_rows_that_do_not_count(n, weight, itype):
+    """Negative targets with an infinite or NaN weight (mask / mask.sum() of an
+    answer that is masked throughout): the loss is that of the other rows."""
+    x, y, g = rows(n, 50, torch.float32, 5)
+    y[::3] = -1
+    old = exact(x, y)[0].float() + 0.1
+    adv = torch.randn(n, generator=g, device="cuda")
+    w = torch.rand(n, generator=g, device="cuda")
+    got = []
+    for bad in (0.0, weight):
+        w[::3] = bad
+        loss, token = torch.empty(1, device="cuda"), torch.empty(n, device="cuda")
+        out = torch.empty_like(x)
+        O.z1_policy_loss(x, y.to(itype), old, adv, loss=loss, token_loss=token, dlogits=out, weights=w, scale=0.5)
+        got.append((loss, token, out))
+    assert torch.isfinite(got[0][0]).all()
+    assert all(torch.equal(a, b) for a, b in zip(*got))
