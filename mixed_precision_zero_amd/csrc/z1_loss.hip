@@ -226,16 +226,29 @@ __device__ __forceinline__ Stat row_stat(const Cut<T> &c, float *lds, Pack16<T> 
     return block_stat<NT>(a, lds);
 }
 
+// log sum_v exp x_v in two parts: the row's maximum, and the binary logarithm
+// of what its exponentials sum to when taken from there.  x - top is rounded at
+// the size of the row's spread, where x less a sum of both would be off by that
+// sum's rounding, 5e-4 of every probability for logits around 1e4.
+struct Lse {
+    float top, log2s;
+    // exp(x - lse)
+    __device__ __forceinline__ float prob(float x) const
+    {
+        return __builtin_amdgcn_exp2f(fmaf(x - top, kLog2e, -log2s));
+    }
+};
+
 // -d exp(x - lse), and d more at the target.
 template <typename T>
 __device__ __forceinline__ Pack16<T> grad_vec(const Pack16<T> &p, int64_t at, int64_t y, float d,
-                                              float lse)
+                                              Lse lse)
 {
     Pack16<T> g;
     float f[Pack16<T>::N];
 #pragma unroll
     for (int k = 0; k < Pack16<T>::N; ++k)
-        f[k] = -d * fast_exp(T::up(p.e[k]) - lse);
+        f[k] = -d * lse.prob(T::up(p.e[k]));
     if (y >= at && y < at + Pack16<T>::N) {
 #pragma unroll
         for (int k = 0; k < Pack16<T>::N; ++k)
@@ -249,13 +262,13 @@ __device__ __forceinline__ Pack16<T> grad_vec(const Pack16<T> &p, int64_t at, in
 }
 
 template <typename T, int NT>
-__device__ __forceinline__ void grad_edges(const Cut<T> &c, int64_t y, float d, float lse)
+__device__ __forceinline__ void grad_edges(const Cut<T> &c, int64_t y, float d, Lse lse)
 {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
         const int64_t i = c.edge(e);
         if (i >= 0) {
-            float f = -d * fast_exp(T::up(c.x[i]) - lse);
+            float f = -d * lse.prob(T::up(c.x[i]));
             if (i == y)
                 f += d;
             c.d[i] = T::down(f);
@@ -265,7 +278,7 @@ __device__ __forceinline__ void grad_edges(const Cut<T> &c, int64_t y, float d, 
 
 // Vectors first .. end - 1 of the row, and with the first of them its edges.
 template <typename T, int NT>
-__device__ __forceinline__ void stream_grad(const Cut<T> &c, int64_t y, float d, float lse,
+__device__ __forceinline__ void stream_grad(const Cut<T> &c, int64_t y, float d, Lse lse,
                                             int64_t first, int64_t end)
 {
     constexpr int N = Pack16<T>::N;
@@ -348,7 +361,7 @@ __global__ __launch_bounds__(NT) void k_logprob_grad(Rows r, int64_t row0, const
         return;
     }
     const float d = y < r.vocab ? dlogp[row] : __builtin_nanf("");
-    stream_grad<T, NT>(c, y, d, lse[row], first, end);
+    stream_grad<T, NT>(c, y, d, Lse{lse[row], 0.f}, first, end);
 }
 
 // Loss of one counted row and its slope in logp.
@@ -379,7 +392,7 @@ template <typename T, int NT, int NV>
 __global__ __launch_bounds__(NT) void k_policy(Rows r, int64_t row0, PolicyPtrs p, PolicyScalars k)
 {
     __shared__ float lds[2 * NT / 64];
-    __shared__ float shared[2];
+    __shared__ float shared[3];
     const int64_t row = row0 + blockIdx.x;
     const int64_t y = target_of(r, row);
     const float w = p.w ? p.w[row] : 1.f;
@@ -410,12 +423,14 @@ __global__ __launch_bounds__(NT) void k_policy(Rows r, int64_t row0, PolicyPtrs 
         if (p.logp)
             p.logp[row] = logp;
         shared[0] = slope * w * k.scale;
-        shared[1] = a.base() + logs;
+        shared[1] = a.base();
+        shared[2] = logs * kLog2e;
     }
     if (!c.d)
         return;
     __syncthreads();
-    const float d = shared[0], lse = shared[1];
+    const float d = shared[0];
+    const Lse lse{shared[1], shared[2]};
     if (NV > 0) {
 #pragma unroll
         for (int q = 0; q < NV; ++q) {
@@ -427,7 +442,7 @@ __global__ __launch_bounds__(NT) void k_policy(Rows r, int64_t row0, PolicyPtrs 
         for (int e = 0; e < 2; ++e) {
             const int64_t i = c.edge(e);
             if (i >= 0) {
-                float f = -d * fast_exp(edge[e] - lse);
+                float f = -d * lse.prob(edge[e]);
                 if (i == y)
                     f += d;
                 c.d[i] = T::down(f);

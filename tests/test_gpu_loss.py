@@ -359,3 +359,36 @@ def test_weights_of_rows_that_do_not_count(n, weight, itype):
         got.append((loss, token, out))
     assert torch.isfinite(got[0][0]).all()
     assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
+def shifted(n, V, dtype, shift):
+    """Logits around `shift` with the spread that `rows` has, or (None) the
+    type's lowest value throughout."""
+    x, y, g = rows(n, V, torch.float32, V + 7)
+    y.clamp_(min=0)
+    x = torch.full_like(x, torch.finfo(dtype).min) if shift is None else x + shift
+    return x.to(dtype), y, g
+
+
+SHIFTS = [1e3, -1e3, 1e4, -1e4, 1e6, None]
+
+
+@pytest.mark.parametrize("dtype,shift", [(d, s) for d in DT for s in SHIFTS if not (d == torch.float16 and s == 1e6)], ids=str)
+@pytest.mark.parametrize("n,V", [(6, 100), (5, 2049), (3, 32001), (2, 100001)])
+def test_policy_gradient_far_from_zero(n, V, dtype, shift):
+    """A constant added to a row changes no probability: the bounds are those
+    of rows around zero, whose spread alone counts."""
+    x, y, g = shifted(n, V, dtype, shift)
+    z = x.double() - x.double().amax(1, keepdim=True)
+    wp, wl, _ = exact(z, y)
+    old = wp.float()
+    adv = torch.randn(n, generator=g, device="cuda")
+    loss, token, logp, out = (torch.empty(1, device="cuda"), torch.empty(n, device="cuda"),
+                              torch.empty(n, device="cuda"), torch.empty_like(x))
+    O.z1_policy_loss(x, y, old, adv, loss=loss, token_loss=token, logp=logp, dlogits=out)
+    assert ((logp.double() - wp).abs() <= LOGP).all()
+    d = -torch.exp(logp.double() - old.double()) * adv.double()    # the ratio is 1 to a few roundings
+    want, d = exact_grad(z, y, wl, d)
+    check_grad(out, want, d, 3 * LOGP)
+    O.z1_policy_loss(x, y, old, adv, loss=loss, token_loss=token, dlogits=x)
+    assert torch.equal(x, out)
