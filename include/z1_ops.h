@@ -164,7 +164,10 @@ z1_status z1_token_logprob(const z1_logits *x, float *logp, float *lse, z1_strea
 
 /* dlogits_rv = dlogp_r (1[v == y_r] - exp(x_rv - lse_r)), rounded once to
  * dtype, ld_d elements between rows; dlogits may be the logits themselves
- * (with the same row distance, else Z1_EINVAL), but not overlap them otherwise. */
+ * (with the same row distance, else Z1_EINVAL), but not overlap them otherwise.
+ * Where |lse| is 64 or more, and is the row's own as z1_token_logprob gave it,
+ * the exponent is taken from the row's maximum and log-sum anew (one more
+ * read of that row), so that lse's rounding does not reach the gradient. */
 z1_status z1_logprob_grad(const z1_logits *x, const float *lse, const float *dlogp,
                           void *dlogits, int64_t ld_d, z1_stream stream);
 

@@ -15,7 +15,7 @@
 //     out, past the caches (4096 x 49152 bf16: 142 us, 5.7 TB/s both ways;
 //     157 with ordinary stores, 173 with 1024 lanes a row, 152 with 256);
 //   - z1_logprob_grad is one pass from logits to gradient (6144 x 32000 bf16:
-//     114 us, 6.9 TB/s, part of it from cache).
+//     114 us, 6.9 TB/s, part of it from cache), and two for rows far from zero.
 // Maxima, sums, log-probabilities and losses are fp32 or wider; the gradient
 // is rounded once, to the logits' type.
 #include "z1_ops_internal.h"
@@ -342,6 +342,11 @@ __global__ __launch_bounds__(NT) void k_logprob(Rows r, int64_t row0, float *log
     }
 }
 
+// From this |lse| on z1_logprob_grad takes a row's maximum and log-sum anew.
+// Below it lse's own rounding is at most 2^-19 of a probability, no more than
+// the exponent's for one of e^-22.
+constexpr float kFarLse = 64.f;
+
 // The last rows first: z1_token_logprob has just read the logits front to
 // back, and the end of them is still in the 256 MB memory-side cache (6144 x
 // 32000 bf16, both kernels and the pairs': 189 us, front to back 208).
@@ -349,10 +354,11 @@ template <typename T, int NT>
 __global__ __launch_bounds__(NT) void k_logprob_grad(Rows r, int64_t row0, const float *lse,
                                                     const float *dlogp)
 {
+    __shared__ float lds[2 * NT / 64];
     const int64_t row = row0 + gridDim.x - 1 - blockIdx.x;
     const int64_t y = target_of(r, row);
     const Cut<T> c(r, row);
-    const int64_t first = c.nvec * blockIdx.y / gridDim.y, end = c.nvec * (blockIdx.y + 1) / gridDim.y;
+    int64_t first = c.nvec * blockIdx.y / gridDim.y, end = c.nvec * (blockIdx.y + 1) / gridDim.y;
     // a piece without vectors has nothing to do, unless it is the first
     if (blockIdx.y > 0 && first == 0)
         return;
@@ -361,7 +367,21 @@ __global__ __launch_bounds__(NT) void k_logprob_grad(Rows r, int64_t row0, const
         return;
     }
     const float d = y < r.vocab ? dlogp[row] : __builtin_nanf("");
-    stream_grad<T, NT>(c, y, d, Lse{lse[row], 0.f}, first, end);
+    Lse l{lse[row], 0.f};
+    if (fabsf(l.top) >= kFarLse) {
+        // a far row is one workgroup's, for it has to be read whole before any
+        // of it is overwritten (dlogits may be the logits); an lse that is not
+        // the row's own to a unit or two in its last place is taken as it is
+        if (blockIdx.y > 0)
+            return;
+        first = 0;
+        end = c.nvec;
+        const Stat a = stream_stat<T, NT>(c, lds);
+        const float logs = logf(a.s);
+        if (fabsf((a.base() + logs) - l.top) < fabsf(l.top) * 0x1p-22f)
+            l = Lse{a.base(), logs * kLog2e};
+    }
+    stream_grad<T, NT>(c, y, d, l, first, end);
 }
 
 // Loss of one counted row and its slope in logp.

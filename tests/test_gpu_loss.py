@@ -392,3 +392,44 @@ def test_policy_gradient_far_from_zero(n, V, dtype, shift):
     check_grad(out, want, d, 3 * LOGP)
     O.z1_policy_loss(x, y, old, adv, loss=loss, token_loss=token, dlogits=x)
     assert torch.equal(x, out)
+
+
+@pytest.mark.parametrize("dtype,shift", [(d, s) for d in DT for s in SHIFTS if not (d == torch.float16 and s == 1e6)], ids=str)
+@pytest.mark.parametrize("n,V", [(6, 100), (5, 2049), (3, 32001), (2, 100001)])
+def test_logprob_gradient_far_from_zero(n, V, dtype, shift):
+    """As for the policy gradient, through the fp32 lse, which alone is rounded
+    at its own size."""
+    x, y, g = shifted(n, V, dtype, shift)
+    z = x.double() - x.double().amax(1, keepdim=True)
+    wp, wl, _ = exact(z, y)
+    logp, lse, out = torch.empty(n, device="cuda"), torch.empty(n, device="cuda"), torch.empty_like(x)
+    O.z1_token_logprob(x, y, logp, lse)
+    assert ((logp.double() - wp).abs() <= LOGP).all()
+    true = x.double().amax(1) + wl
+    assert ((lse.double() - true).abs() <= LOGP + true.abs() * 2.0 ** -24).all()
+    d = torch.randn(n, generator=g, device="cuda")
+    O.z1_logprob_grad(x, y, lse, d, out)
+    want, dd = exact_grad(z, y, wl, d)
+    check_grad(out, want, dd)
+    O.z1_logprob_grad(x, y, lse, d, x)
+    assert torch.equal(x, out)
+
+
+@pytest.mark.parametrize("n,V", [(6, 100), (2, 100001)])
+def test_logprob_gradient_takes_another_lse_as_it_is(n, V):
+    """An lse that is not the row's own: exp(x - lse) with it, also far from
+    zero, where x - lse is exact here (integers below 2^24)."""
+    g = torch.Generator(device="cuda").manual_seed(V)
+    x = torch.randint(990, 1000, (n, V), generator=g, device="cuda").float()
+    y = torch.randint(0, V, (n,), generator=g, device="cuda")
+    lse, d = torch.full((n,), 1005.0, device="cuda"), torch.randn(n, generator=g, device="cuda")
+    out = torch.empty_like(x)
+    O.z1_logprob_grad(x, y, lse, d, out)
+    want, dd = exact_grad(x, y, lse, d)
+    check_grad(out, want, dd)
+    # infinite and NaN ones
+    for odd, p in ((math.inf, 0.0), (math.nan, math.nan)):
+        lse.fill_(odd)
+        O.z1_logprob_grad(x, y, lse, torch.ones_like(d), out)
+        assert torch.equal(out[0, y[0]].isnan(), torch.tensor(math.isnan(p), device="cuda"))
+        assert float(out.nan_to_num(7.0).min()) == (0.0 if p == 0.0 else 7.0)
