@@ -338,7 +338,7 @@ __global__ __launch_bounds__(NT) void k_logprob(Rows r, int64_t row0, float *log
         const float logs = logf(a.s);
         logp[row] = (xy - a.base()) - logs;
         if (lse)
-            lse[row] = a.base() + logs;
+            lse[row] = y < r.vocab ? a.base() + logs : __builtin_nanf("");
     }
 }
 

@@ -433,3 +433,15 @@ def test_logprob_gradient_takes_another_lse_as_it_is(n, V):
         O.z1_logprob_grad(x, y, lse, torch.ones_like(d), out)
         assert torch.equal(out[0, y[0]].isnan(), torch.tensor(math.isnan(p), device="cuda"))
         assert float(out.nan_to_num(7.0).min()) == (0.0 if p == 0.0 else 7.0)
+
+
+@pytest.mark.parametrize("V", [5, 5000, 100001])
+def test_ids_past_the_vocabulary_have_no_lse(V):
+    """NaN in all of their outputs; the rows beside them keep theirs."""
+    x, y, g = rows(4, V, torch.float32, V)
+    y[:] = torch.tensor([V, 0, -1, V + 9], device="cuda")
+    logp, lse = torch.zeros(4, device="cuda"), torch.zeros(4, device="cuda")
+    O.z1_token_logprob(x, y, logp, lse)
+    for out in (logp, lse):
+        assert out.isnan().tolist() == [True, False, False, True] and float(out[2]) == 0.0
+    assert abs(float(lse[1]) - float(exact(x, y.clamp(max=V - 1))[1][1])) <= LOGP
