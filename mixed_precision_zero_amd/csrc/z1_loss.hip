@@ -553,7 +553,8 @@ __global__ __launch_bounds__(256) void k_preference(z1_preference_args a)
     if (threadIdx.x == 0) {
         const double soft = log1p(t);
         const double down = soft + (z < 0.0 ? -z : 0.0), up = soft + (z > 0.0 ? z : 0.0);
-        a.pair_loss[p] = (float)((1.0 - e) * down + (e != 0.0 ? e * up : 0.0));
+        // a side of weight 0 adds nothing, infinite or not
+        a.pair_loss[p] = (float)((e != 1.0 ? (1.0 - e) * down : 0.0) + (e != 0.0 ? e * up : 0.0));
         if (a.margins)
             a.margins[p] = (float)z;
     }

@@ -445,3 +445,18 @@ def test_ids_past_the_vocabulary_have_no_lse(V):
     for out in (logp, lse):
         assert out.isnan().tolist() == [True, False, False, True] and float(out[2]) == 0.0
     assert abs(float(lse[1]) - float(exact(x, y.clamp(max=V - 1))[1][1])) <= LOGP
+
+
+@pytest.mark.parametrize("e,z,want", [(1.0, -math.inf, 0.0), (1.0, math.inf, math.inf), (0.0, math.inf, 0.0),
+                                      (0.0, -math.inf, math.inf), (0.5, math.inf, math.inf)])
+def test_preference_of_infinite_margins(e, z, want):
+    """A target whose logit is masked has log-probability -inf: the side of the
+    loss that smoothing gives no weight does not count."""
+    logp = torch.tensor([z, 0.0] if z < 0 else [0.0, -z], device="cuda")
+    zero, y = torch.zeros(2, device="cuda"), torch.zeros(2, dtype=torch.long, device="cuda")
+    loss, pair, d = torch.empty(1, device="cuda"), torch.empty(1, device="cuda"), torch.empty(2, device="cuda")
+    O.z1_preference_loss(logp, zero, y, torch.tensor([0, 1, 2], device="cuda"), beta=0.5, label_smoothing=e, loss=loss,
+                         pair_loss=pair, dlogp=d)
+    assert float(pair) == want and float(loss) == want
+    slope = 0.5 * (e - 1.0 if z < 0 else e)
+    assert d.tolist() == [slope, -slope]
