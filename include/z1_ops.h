@@ -176,8 +176,8 @@ z1_status z1_logprob_grad(const z1_logits *x, const float *lse, const float *dlo
  *   l   = -min(rho A, clamp(rho, 1 - clip_low, 1 + clip_high) A)
  *         + kl_coef (exp(ref - logp) - (ref - logp) - 1)
  *   loss = scale * sum_r w_r l_r      dlogits = d loss / d logits
- * token_loss gets l_r (0 where not counted).  ref_logp may be NULL (no KL
- * term), weights NULL (all 1), dlogits NULL (no gradient), logp NULL;
+ * token_loss gets l_r (0 where not counted).  ref_logp may be NULL and kl_coef 0
+ * (either: no KL term, and ref_logp is not read), weights NULL (all 1), dlogits NULL (no gradient), logp NULL;
  * dlogits may be the logits themselves, as above.  Where the minimum's two sides are
  * equal with rho outside the clamp (A = 0), the gradient is the clamp's. */
 typedef struct z1_policy_args {

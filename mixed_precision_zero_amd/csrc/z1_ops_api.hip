@@ -674,7 +674,10 @@ z1_status z1_policy_loss(const z1_logits *x, const z1_policy_args *a, z1_stream 
         return Z1_EALIGN;
     if (!runs_on(current_device(), stream))
         return Z1_EINVAL;
-    const z1::ops::PolicyPtrs p{a->old_logp, a->ref_logp, a->advantages, a->weights, a->token_loss, a->logp};
+    // without a coefficient there is no KL term: 0 times what overflows in it
+    // would be NaN
+    const float *ref = (float)a->kl_coef != 0.f ? a->ref_logp : nullptr;
+    const z1::ops::PolicyPtrs p{a->old_logp, ref, a->advantages, a->weights, a->token_loss, a->logp};
     const z1::ops::PolicyScalars k{(float)(1.0 - a->clip_low), (float)(1.0 + a->clip_high),
                                    (float)a->kl_coef, (float)a->scale};
     return z1::ops::launch_policy(x->dtype, r, p, k, a->loss, a->scale,

@@ -362,7 +362,7 @@ def z1_policy_loss(logits, targets, old_logp, advantages, *, loss, token_loss, l
                    dlogits=None, ref_logp=None, weights=None, clip_low: float = 0.2,
                    clip_high: float = 0.2, kl_coef: float = 0.0, scale: float = 1.0,
                    stream=None) -> None:
-    """Clipped policy loss with a KL term to ref_logp (None: no such term):
+    """Clipped policy loss with a KL term to ref_logp (None, or kl_coef 0: no such term):
     loss[0] = scale * sum of weights * token_loss, and dlogits (None: no
     gradient) its gradient in the logits.  Rows with a negative target or a
     zero weight count for nothing.  dlogits may be logits."""

@@ -460,3 +460,19 @@ def test_preference_of_infinite_margins(e, z, want):
     assert float(pair) == want and float(loss) == want
     slope = 0.5 * (e - 1.0 if z < 0 else e)
     assert d.tolist() == [slope, -slope]
+
+
+def test_no_kl_coefficient_no_kl_term():
+    """kl_coef 0: whatever the reference holds, exp(ref - logp) past fp32's
+    range and NaN among it, the result is that without a reference."""
+    x, y, g = rows(30, 200, torch.float32, 3)
+    old, adv = exact(x, y)[0].float(), torch.randn(30, generator=g, device="cuda")
+    ref = old + 100.0
+    ref[::4] = float("nan")
+    got = []
+    for r in (None, ref):
+        loss, token, out = torch.empty(1, device="cuda"), torch.empty(30, device="cuda"), torch.empty_like(x)
+        O.z1_policy_loss(x, y, old, adv, loss=loss, token_loss=token, dlogits=out, ref_logp=r, kl_coef=0.0)
+        got.append((loss, token, out))
+    assert torch.isfinite(got[0][0]).all() and torch.isfinite(got[0][2]).all()
+    assert all(torch.equal(a, b) for a, b in zip(*got))
