@@ -178,6 +178,20 @@ def _dptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
+def _memory(*bound):
+    """The memory of every tensor among `bound` (tensors, device addresses,
+    None, and lists of them): what a handle with device addresses has to hold
+    on to.  Not the caller's lists or tensors, which may be emptied or given
+    other memory while the handle lives."""
+    held = []
+    for x in bound:
+        if isinstance(x, torch.Tensor):
+            held.append(x.untyped_storage())
+        elif isinstance(x, (list, tuple)):
+            held += _memory(*x)
+    return tuple(held)
+
+
 def _check_tensors(items) -> None:
     """Reject tensors the library would read or write out of bounds or
     misread.  items: (tensor, name, dtype, min_elems) with dtype None meaning

@@ -287,3 +287,43 @@ def test_binding_refuses_loss_tensors():
         O.z1_preference_loss(v.double(), v, y, cu, beta=0.1, loss=v, pair_loss=v)
     with pytest.raises(ValueError, match="ref_logp"):
         O.z1_preference_loss(v, v[:2], y, cu, beta=0.1, loss=v, pair_loss=v)
+
+
+class Lib:
+    """The library's create and destroy without a GPU: each handle is an
+    address."""
+
+    def __getattr__(self, name):
+        def call(out, *args):
+            if name.endswith("create"):
+                out._obj.value = 0x1000
+            return B.Z1_OK
+        return call
+
+
+def on_host_memory(shape, dtype, alive):
+    """A tensor over a numpy array, which `alive` watches."""
+    import weakref
+    import numpy as np
+    a = np.zeros(shape, dtype=np.int32 if dtype == torch.float32 else np.int16)
+    alive.append(weakref.ref(a))
+    return torch.from_numpy(a).view(dtype)
+
+
+def test_muon_holds_the_memory_it_is_bound_to(monkeypatch):
+    """Not the caller's lists: emptied, or their tensors given other memory
+    (as p.data = x does), they leave the handle's addresses valid until close."""
+    monkeypatch.setattr(O, "lib", Lib())
+    monkeypatch.setattr(O, "_on_gpu", lambda items: None)
+    monkeypatch.setattr(O, "_stream", lambda stream: None)
+    alive = []
+    make = lambda dtype: [on_host_memory((4, 6), dtype, alive), on_host_memory((3, 5), dtype, alive)]  # noqa: E731
+    lists = [make(t) for t in (torch.float32, torch.float32, torch.float32, torch.bfloat16, torch.bfloat16)]
+    grads, momentum, master, weights, ortho = lists
+    m = O.z1_muon_create([(4, 6), (3, 5)], grads, momentum=momentum, master=master, weights=weights, ortho=ortho)
+    master[0].data = torch.zeros(4, 6)
+    for x in lists:
+        x.clear()
+    assert all(r() is not None for r in alive) and len(alive) == 10
+    m.close()
+    assert all(r() is None for r in alive)
