@@ -178,18 +178,16 @@ def _dptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
-def _memory(*bound):
-    """The memory of every tensor among `bound` (tensors, device addresses,
-    None, and lists of them): what a handle with device addresses has to hold
-    on to.  Not the caller's lists or tensors, which may be emptied or given
+def _held(x):
+    """x (a tensor, a device address, None, or a list of them) for a handle
+    with device addresses to hold on to: tensors of its own over the same
+    memory, not the caller's lists or tensors, which may be emptied or given
     other memory while the handle lives."""
-    held = []
-    for x in bound:
-        if isinstance(x, torch.Tensor):
-            held.append(x.untyped_storage())
-        elif isinstance(x, (list, tuple)):
-            held += _memory(*x)
-    return tuple(held)
+    if isinstance(x, torch.Tensor):
+        return x.detach()
+    if x is None or isinstance(x, int) or hasattr(x, "data_ptr"):
+        return x
+    return tuple(_held(y) for y in x)
 
 
 def _check_tensors(items) -> None:
@@ -265,9 +263,9 @@ class Plan:
     def __init__(self, handle: int, info: PlanInfo, keep):
         self.handle = handle
         self.info = info
-        # the host arrays the bind pointed at and the bound device tensors:
-        # the plan writes into those tensors until it is destroyed, so they
-        # must not return to torch's allocator before it is
+        # the host arrays the bind pointed at and the bound device tensors'
+        # memory: the plan writes into it until it is destroyed, so it must
+        # not return to torch's allocator before it is
         self._keep = keep
 
     def close(self):
@@ -359,8 +357,8 @@ def z1_plan_create(numel: Sequence[int], dp_size: int, rank: int, weights: Seque
            "z1_plan_create")
     info = PlanInfo()
     _check(lib.z1_plan_query(h, ctypes.byref(info)), "z1_plan_query")
-    return Plan(h.value, info, (n, wp, gp, r, ls, ws, weights, grads, master, exp_avg,
-                                exp_avg_sq, acc))
+    return Plan(h.value, info, (n, wp, gp, r, ls, ws) +
+                _held((weights, grads, master, exp_avg, exp_avg_sq, acc)))
 
 
 def z1_plan_layout(plan: Plan):
@@ -497,7 +495,7 @@ class Pack:
     def __init__(self, handle: int, seg: int, keep):
         self.handle = handle
         self.seg = seg
-        self._keep = keep   # host arrays and the bound device tensors (as Plan)
+        self._keep = keep   # host arrays and the bound device tensors' memory (as Plan)
 
     def close(self):
         if self.handle:
@@ -536,7 +534,7 @@ def z1_pack_create(numel: Sequence[int], dp_size: int, grads: Sequence[Sequence]
     h = ctypes.c_void_p()
     _check(lib.z1_pack_create(ctypes.byref(h), ctypes.byref(b), _stream(stream)), "z1_pack_create")
     seg = z1_pack_layout(n, dp_size, kind, r)
-    return Pack(h.value, seg, (n, r, gp, grads, send))
+    return Pack(h.value, seg, (n, r, gp) + _held((grads, send)))
 
 
 def z1_pack_accum(pack: Pack, k: int, stream=None) -> None:

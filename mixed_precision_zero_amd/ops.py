@@ -13,7 +13,7 @@ from typing import Optional, Sequence
 import numpy as np
 import torch
 
-from .binding import LIB_PATH, _check, _dptr, _memory, _p64, _stream as _any_stream, lib
+from .binding import LIB_PATH, _check, _dptr, _held, _p64, _stream as _any_stream, lib
 
 EXPORTS = ("z1_ops_abi_version", "z1_muon_create", "z1_muon_destroy", "z1_muon_step",
            "z1_muon_orthogonalize", "z1_embed_lookup", "z1_embed_grad_workspace",
@@ -191,7 +191,7 @@ class Muon:
     def __init__(self, handle: int, n: int, keep):
         self.handle = handle
         self.n = n
-        self._keep = keep   # the bound tensors' memory: the handle writes into it until it is destroyed
+        self._keep = keep   # the bound memory: the handle writes into it until it is destroyed
 
     def close(self):
         if self.handle:
@@ -252,7 +252,7 @@ def z1_muon_create(shapes: Sequence, grads: Sequence, *, momentum: Optional[Sequ
                  c=float(coeffs[2]), eps=float(eps), ns_steps=int(ns_steps), reserved=0)
     h = ctypes.c_void_p()
     _check(lib.z1_muon_create(ctypes.byref(h), ctypes.byref(b), _stream(stream)), "z1_muon_create")
-    return Muon(h.value, n, _memory(*lists.values()))
+    return Muon(h.value, n, _held(tuple(lists.values())))
 
 
 def z1_muon_step(muon: Muon, *, lr: float, momentum: float = 0.95, weight_decay: float = 0.0,

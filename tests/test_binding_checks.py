@@ -186,3 +186,79 @@ def test_norm_flat_noalloc_host_checks():
     assert L.z1_grad_norm_sq_flat_noalloc(0x1000, 5, 0x2004, None) == B.Z1_EALIGN
     with pytest.raises(ValueError, match="acc: 9 elements"):
         B.z1_grad_norm_sq_flat_noalloc(torch.zeros(9), 10, torch.zeros(1, dtype=torch.float64))
+
+
+# ------------------------------------------------- what a handle holds on to
+
+class _Lib:
+    """The library without a GPU: host calls go to it, and each handle is an
+    address."""
+
+    def __getattr__(self, name):
+        if name.endswith(("_create", "_destroy", "_query")):
+            def call(out, *args):
+                if name.endswith("_create"):
+                    out._obj.value = 0x1000
+                return B.Z1_OK
+            return call
+        return getattr(_REAL, name)
+
+
+_REAL = B.lib
+
+
+def _watched(n, dtype, alive):
+    """A tensor over a numpy array, which `alive` watches."""
+    import weakref
+    import numpy as np
+    a = np.zeros(n, dtype=np.int32 if dtype == torch.float32 else np.int16)
+    alive.append(weakref.ref(a))
+    return torch.from_numpy(a).view(dtype)
+
+
+@pytest.fixture
+def no_gpu(monkeypatch):
+    monkeypatch.setattr(B, "lib", _Lib())
+    monkeypatch.setattr(B, "_check_tensors", lambda items: None)
+    monkeypatch.setattr(B, "_stream", lambda stream: None)
+
+
+@pytest.mark.parametrize("layout", ["full", "packed"])
+def test_plan_holds_the_memory_it_is_bound_to(layout, no_gpu):
+    """Not the caller's lists: emptied, or their tensors given other memory
+    (as p.data = x does), they leave the plan's addresses valid until close."""
+    alive, bf = [], torch.bfloat16
+    args, A = _plan_args(layout)
+    for name in ("master", "exp_avg", "exp_avg_sq", "acc"):
+        args[name] = _watched(A, torch.float32, alive)
+    if layout == "packed":
+        weights, grads = _watched(A, bf, alive), [_watched(A, bf, alive) for _ in range(K)]
+    else:
+        weights = [_watched(n, bf, alive) for n in NUMEL]
+        grads = [[_watched(n, bf, alive) for n in NUMEL] for _ in range(K)]
+    plan = B.z1_plan_create(**dict(args, weights=weights, grads=grads))
+    if layout == "full":
+        weights[1].data = torch.zeros(NUMEL[1], dtype=bf)
+        weights.clear()
+        for gk in grads:
+            gk.clear()
+    grads.clear()
+    args.clear()
+    del weights
+    assert all(r() is not None for r in alive)
+    plan.close()
+    assert all(r() is None for r in alive)
+
+
+def test_pack_holds_the_memory_it_is_bound_to(no_gpu):
+    alive = []
+    grads = [[_watched(n, torch.bfloat16, alive) for n in NUMEL] for _ in range(K)]
+    send = _watched(D * B.z1_pack_layout(NUMEL, D), torch.float32, alive)
+    pack = B.z1_pack_create(NUMEL, D, grads, send)
+    send.data = torch.zeros(1)
+    for gk in grads:
+        gk.clear()
+    grads.clear()
+    assert all(r() is not None for r in alive)
+    pack.close()
+    assert all(r() is None for r in alive)
