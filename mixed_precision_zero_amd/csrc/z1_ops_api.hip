@@ -16,6 +16,8 @@ using z1::ops::MuonMat;
 using z1::ops::MuonTables;
 using z1::ops::MuonTile;
 using z1::ops::MuonUpdate;
+using z1::ops::pad_to;
+using z1::ops::pick_tile;
 
 struct z1_muon {
     int device = -1;
@@ -127,55 +129,6 @@ bool coefficients_ok(const z1_muon_bind *b)
             return false;
     }
     return true;
-}
-
-int64_t pad_to(int64_t x, int64_t q) { return (x + q - 1) / q * q; }
-
-// The tile side a product runs with (0: X X^T, 1: A A, 2: B X): the one with
-// the smallest estimate of its time,
-//   fixed + panels * (time of a 32-deep panel)   microseconds,
-// where r = ceil(tiles / 256) tiles fall to the busiest compute unit and a
-// panel takes 0.1 r for tiles of 64, max(0.43, 0.36 r - 0.3) for 128 (which
-// overlap two or three to a unit) and 0.68, or 0.88 r from two on, for 256
-// (one to a unit).  Measured (64 / 128 / 256, us): whole calls 2 x 333 x 1537
-// 130 / 238 / 493, 4 x 1024^2 249 / 298 / 523, 1 x 2048^2 388 / 441 / 777,
-// 24 x 2048^2 7936 / 6364 / 5551; single products of 2 x 2048 x 8192
-// (128 / 256) 112 / 157, 34 / 53 and 207 / 181, of 4 x 2048^2 62 / 62, 63 / 65
-// and 113 / 87, of 4096 x 11008 245 / 250, 99 / 104 and 472 / 401.
-int pick_tile(int product, int32_t n, const int64_t *rows, const int64_t *cols)
-{
-#ifdef Z1_MUON_TILE
-    return Z1_MUON_TILE;   // for measuring one side against another
-#endif
-    static const struct {
-        int side;
-        double fixed;
-    } kTiles[3] = {{64, 3.0}, {128, 6.0}, {256, 13.0}};
-    int tile = 64;
-    double best = 0.0;
-    for (const auto &c : kTiles) {
-        double tiles = 0.0, work = 0.0;
-        for (int32_t i = 0; i < n; ++i) {
-            const double m = (double)pad_to(std::min(rows[i], cols[i]), c.side);
-            const double w = (double)pad_to(std::max(rows[i], cols[i]), c.side);
-            const double q = m / c.side;
-            const double t = product == 2 ? q * (w / c.side) : q * (q + 1) / 2;
-            tiles += t;
-            work += t * (product == 0 ? w : m) / 32;
-        }
-        if (n == 0)
-            break;
-        const double r = ceil(tiles / 256.0);
-        const double panel = c.side == 64 ? 0.1 * r
-                             : c.side == 128 ? std::max(0.43, 0.36 * r - 0.3)
-                                             : (r > 1.0 ? 0.88 * r : 0.68);
-        const double cost = c.fixed + work / tiles * panel;
-        if (c.side == 64 || cost < best) {
-            best = cost;
-            tile = c.side;
-        }
-    }
-    return tile;
 }
 
 // Spreads a list of tiles over the 8 XCDs: workgroup p runs on XCD p mod 8,
@@ -316,20 +269,11 @@ z1_status muon_create(z1_muon **out, const z1_muon_bind *b, z1_stream stream)
         for (int p = 0; p < 3; ++p)
             add_tiles(tiles[p], at, q.mp / t.tile[p], (p == 2 ? q.np : q.mp) / t.tile[p], p < 2);
     }
-    // X X^T of few tiles leaves most of the GPU idle while a few compute units
-    // read long panels: split the depth, at least 16 panels a piece, where
-    // what is saved is more than the join's 3 us (512 x 8192: 290 -> 189 us,
-    // 333 x 1537: 108 -> 103).
     std::vector<MuonTile> pieces;
-    t.splits = 1;
-    if (t.tile[0] == 64 && !tiles[0].empty() && tiles[0].size() <= 128) {
-        int64_t panels = INT64_MAX;
-        for (int32_t at = 0; at < t.n; ++at)
-            panels = std::min<int64_t>(panels, mats[(size_t)at].np / 32);
-        const int64_t s = std::min<int64_t>(256 / (int64_t)tiles[0].size(), panels / 16);
-        if (s > 1 && panels >= 48)
-            t.splits = (int32_t)s;
-    }
+    int64_t panels = INT64_MAX;
+    for (int32_t at = 0; at < t.n; ++at)
+        panels = std::min<int64_t>(panels, mats[(size_t)at].np / 32);
+    t.splits = z1::ops::gram_splits(t.tile[0], (int64_t)tiles[0].size(), panels);
     if (t.splits > 1)
         for (const MuonTile &q : tiles[0])
             for (int32_t s = 0; s < t.splits; ++s)

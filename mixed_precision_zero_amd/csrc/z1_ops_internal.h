@@ -10,6 +10,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "z1_muon_tile.h"
 #include "z1_ops.h"
 
 namespace z1 {
@@ -144,17 +145,6 @@ __host__ __device__ __forceinline__ int64_t carry_at(int64_t np, int64_t i, int6
 {
     const int64_t block = (i >> 5) * (np >> 5) + (j >> 5);
     return block * 1024 + ((i & 31) >> 3) * 256 + (((i >> 2) & 1) * 32 + (j & 31)) * 4 + (i & 3);
-}
-
-// A matrix is small when a workgroup of 8 waves holds all of its iteration:
-// sides padded to 32, at most 4 blocks of 32 x 32 a wave, and X, X^T, A and B
-// in LDS with rows 16 bytes longer than their data (so that consecutive rows
-// start on other banks).
-constexpr int kSmallLds = 160 * 1024 - 256;
-__host__ __device__ __forceinline__ bool muon_small(int64_t mp, int64_t np)
-{
-    return mp * np <= 32 * 1024 &&
-           2 * (mp * (np + 8) + np * (mp + 8) + 2 * mp * (mp + 8)) <= kSmallLds;
 }
 
 constexpr int kCastTile = 64;
