@@ -12,8 +12,9 @@
 //     a running maximum and a sum rescaled when it grows;
 //   - z1_policy_loss's gradient needs nothing but the row itself, so it is
 //     taken from the registers, and the logits cross memory once in and once
-//     out, past the caches (4096 x 49152 bf16: 142 us, 5.7 TB/s both ways;
-//     157 with ordinary stores, 173 with 1024 lanes a row, 152 with 256);
+//     out, the gradient's stores past the caches (4096 x 49152 bf16: 142 us,
+//     5.7 TB/s both ways; 157 with ordinary stores, 173 with 1024 lanes a row,
+//     152 with 256);
 //   - z1_logprob_grad is one pass from logits to gradient (6144 x 32000 bf16:
 //     114 us, 6.9 TB/s, part of it from cache), and two for rows far from zero.
 // Maxima, sums, log-probabilities and losses are fp32 or wider; the gradient
@@ -183,7 +184,7 @@ __device__ __forceinline__ Stat stream_stat(const Cut<T> &c, float *lds)
 
 // Statistics of a row, all of whose vectors (NV a lane) and edge elements stay
 // in registers; NV == 0: of a row that is streamed.
-template <typename T, int NT, int NV, bool LAST>
+template <typename T, int NT, int NV>
 __device__ __forceinline__ Stat row_stat(const Cut<T> &c, float *lds, Pack16<T> (&v)[NV > 0 ? NV : 1],
                                          float (&edge)[2])
 {
@@ -332,7 +333,7 @@ __global__ __launch_bounds__(NT) void k_logprob(Rows r, int64_t row0, float *log
     const Cut<T> c(r, row);
     Pack16<T> v[NV > 0 ? NV : 1];
     float edge[2];
-    const Stat a = row_stat<T, NT, NV, false>(c, lds, v, edge);
+    const Stat a = row_stat<T, NT, NV>(c, lds, v, edge);
     if (threadIdx.x == 0) {
         const float xy = y < r.vocab ? T::up(c.x[y]) : __builtin_nanf("");
         const float logs = logf(a.s);
@@ -434,7 +435,7 @@ __global__ __launch_bounds__(NT) void k_policy(Rows r, int64_t row0, PolicyPtrs 
         xy = y < r.vocab ? T::up(c.x[y]) : __builtin_nanf("");
     Pack16<T> v[NV > 0 ? NV : 1];
     float edge[2];
-    const Stat a = row_stat<T, NT, NV, true>(c, lds, v, edge);
+    const Stat a = row_stat<T, NT, NV>(c, lds, v, edge);
     if (threadIdx.x == 0) {
         const float logs = logf(a.s);
         const float logp = (xy - a.base()) - logs;
@@ -593,7 +594,17 @@ void over_rows(int64_t n, int nt, F &&f)
 }
 
 // Lanes and vectors a lane (0: streamed) of the kernels that hold a row in
-// registers: the loads of a whole row are then in flight at once.
+// registers: the loads of a whole row are then in flight at once.  Each stair is
+// the fewest registers that hold its rows, as they cost residency: with 16
+// vectors a lane instead of 12, 6144 vectors take 102 us instead of 78
+// (z1_token_logprob, 4096 x 49152 bf16), with 24 instead of 8, 4096 lose a half.
+// Held / streamed, us, of z1_policy_loss and z1_token_logprob: 6144 vectors
+// (4096 x 49152 bf16) 154 / 190 and 78 / 84; 8192 (4096 x 65536 bf16) 215 / 234
+// and 118 / 87; 12288 (2048 x 98304 bf16) 176 / 167 and 82 / 69, (2048 x 49152
+// fp32) 158 / 155 and 73 / 70; 16032 (2048 x 128256 bf16, 1024 lanes of 16) 216 /
+// 229 and 140 / 88.  So holding a row pays for both up to 6144 vectors and for
+// the policy loss, which reads it twice otherwise, to 8192; 12288 is where it has
+// stopped paying.
 template <typename T, typename F>
 void by_row(int64_t vocab, F &&f)
 {
