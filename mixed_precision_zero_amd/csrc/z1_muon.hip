@@ -22,11 +22,18 @@
 // with elements near 1 / sqrt(m n).  fp16 keeps 11 bits where bf16 keeps 8.
 // X is carried from step to step in 22 bits, as its fp16 operand copy plus an
 // fp16 remainder (fp32 registers in the one-workgroup kernel), and only the
-// products see it rounded to 11: the step multiplies the small singular values by a = 3.44 each
-// time, and with them every rounding of X, so with X itself rounded to fp16 a
-// low-rank U plus 1% noise comes out 4% off (34% with bf16 throughout), and
-// 0.04% with the carry (simulated in binary64 with these roundings,
-// 1024 x 1024; a gaussian U: 0.13% against 0.12% and 0.9%).
+// products see it rounded to 11: the step multiplies the small singular values
+// by a = 3.44 each time, and with them every rounding of X.  Error of O,
+// measured, and simulated in binary64 with these roundings and X carried in 32,
+// 22 or 11 bits: 2048 x 2048 gaussian 1.2e-3; 1.2e-3, 1.2e-3, 1.1e-3, of rank 4
+// plus 1% noise 8e-5; 8e-5, 8e-5, 4.2e-2, 64 x 64 gaussian 2e-3; 2e-3, 2e-3,
+// 1.7e-3, noisy 5e-4; 5e-4, 5e-4, 3.6e-2.  With bf16 operands throughout it is
+// 1% to 34%.
+//
+// Wide products (z1_muon_create_wide) take X, A and B in 22 bits and carry X in
+// fp32: 1.4e-6 and 2.6e-5 for those 2048 x 2048, where fp32 products leave 3.6e-6
+// and 7e-5.  Steps of 4 x 2048^2 2.71 ms against 1.04, 4096 x 11008 10.4 against
+// 3.8, 8 x 1536 x 576 0.55 against 0.26, 2 x 64 x 256 85 us against 28.
 #include "z1_ops_internal.h"
 
 namespace z1 {
@@ -161,7 +168,7 @@ __global__ __launch_bounds__(256) void k_muon_norm(const MuonMat *mats, const do
 
 // X = U / (|U|_F + eps), as the fp16 operands X and Y = X^T and the
 // remainder, one 64 x 64 tile of the padded X per workgroup through LDS.
-template <bool BF, bool STEP>
+template <bool BF, bool STEP, bool WIDE>
 __global__ __launch_bounds__(256) void k_muon_cast(const MuonMat *mats, const MuonTile *tiles,
                                                    const double *inv, const double *partials,
                                                    double eps, MuonUpdate u)
@@ -202,15 +209,29 @@ __global__ __launch_bounds__(256) void k_muon_cast(const MuonMat *mats, const Mu
         }
         *reinterpret_cast<half8 *>(t.X + panel_at(t.mp, i0 + row, j0 + at)) = x;
         *reinterpret_cast<half8 *>(t.Y[0] + panel_at(t.np, j0 + row, i0 + at)) = y;
+        if (WIDE) {
+            for (int k = 0; k < 8; ++k) {
+                x[k] = low_part(lds[row][at + k]);
+                y[k] = low_part(lds[at + k][row]);
+            }
+            *reinterpret_cast<half8 *>(t.Xl + panel_at(t.mp, i0 + row, j0 + at)) = x;
+            *reinterpret_cast<half8 *>(t.Yl[0] + panel_at(t.np, j0 + row, i0 + at)) = y;
+        }
     }
     for (int q = threadIdx.x; q < 1024; q += 256) {
         // 4 rows of one column, lanes in the remainder's order
         const int block = q >> 8, i = (block >> 1) * 32 + ((q >> 6) & 3) * 8 + ((q >> 5) & 1) * 4;
         const int j = (block & 1) * 32 + (q & 31);
         half4 y;
-        for (int k = 0; k < 4; ++k)
-            y[k] = low_part(lds[i + k][j]);
-        *reinterpret_cast<half4 *>(t.L + carry_at(t.np, i0 + i, j0 + j)) = y;
+        float4v f;
+        for (int k = 0; k < 4; ++k) {
+            f[k] = lds[i + k][j];
+            y[k] = low_part(f[k]);
+        }
+        if (WIDE)
+            *reinterpret_cast<float4v *>(t.F + carry_at(t.np, i0 + i, j0 + j)) = f;
+        else
+            *reinterpret_cast<half4 *>(t.L + carry_at(t.np, i0 + i, j0 + j)) = y;
     }
 }
 
@@ -350,7 +371,11 @@ __device__ __forceinline__ void put_block(const MuonMat &t, const MuonUpdate &u,
 // three workgroups a compute unit; 64 tiles take two panels a step, as a step
 // of so few matrix instructions is mostly the wait for its fragments
 // (333 x 1537: 112 us against 137).
-template <int T, int WM, int WN, int PANELS, int RING, bool PAIRED, Mode MODE>
+//
+// WIDE: P = Ph + Pl and Q = Qh + Ql, each half an operand of its own, and the
+// product is Ph Ql + Pl Qh + Ph Qh (Pl Ql is below what 22 bits hold): the
+// panels of three products one after another into the same accumulators.
+template <int T, int WM, int WN, int PANELS, int RING, bool PAIRED, Mode MODE, bool WIDE>
 __global__ __launch_bounds__(64 * WM * WN) void k_muon_gemm(const MuonMat *mats,
                                                             const MuonTile *tiles, int src,
                                                             float ca, float cb, float cc,
@@ -370,32 +395,44 @@ __global__ __launch_bounds__(64 * WM * WN) void k_muon_gemm(const MuonMat *mats,
     const int wm = wave / WN, wn = wave % WN;
     const int i0 = tl.ti * T, j0 = tl.tj * T;
 
-    const _Float16 *P, *Q;
+    const _Float16 *P, *Q, *Pl = nullptr, *Ql = nullptr;
     int64_t p_step, q_step;
     int K;
     if (MODE == kGram || MODE == kGramPart) {
         P = Q = t.X;
+        Pl = Ql = t.Xl;
         K = t.np;
         p_step = q_step = (int64_t)t.mp * 32;
         if (MODE == kGramPart) {   // one of `splits` equal pieces of the depth
             const int piece = (t.np / 64 + splits - 1) / splits * 64;
             const int first = tl.part % splits * piece;
             P = Q = t.X + (int64_t)first * t.mp;
+            Pl = Ql = t.Xl + (int64_t)first * t.mp;
             K = max(0, min(piece, t.np - first));
         }
     } else if (MODE == kPoly) {
         P = Q = t.A;
+        Pl = Ql = t.Al;
         K = t.mp;
         p_step = q_step = (int64_t)t.mp * 32;
     } else {
         P = t.B;
         Q = t.Y[src];
+        Pl = t.Bl;
+        Ql = t.Yl[src];
         K = t.mp;
         p_step = (int64_t)t.mp * 32;
         q_step = (int64_t)t.np * 32;
     }
     P += (int64_t)i0 * 32;
     Q += (int64_t)j0 * 32;
+    const _Float16 *const Ph = P, *const Qh = Q;
+    int left = K / 32, pass = 0;   // panels before the next of the three products
+    if (WIDE) {
+        Pl += (int64_t)i0 * 32;
+        Ql += (int64_t)j0 * 32;
+        Q = Ql;
+    }
     const int voff = ((lane >> 2) * 32 + ((lane & 3) ^ ((lane >> 4) & 3)) * 8) * 2;
 
     typedef __attribute__((address_space(3))) void lds_void;
@@ -413,6 +450,12 @@ __global__ __launch_bounds__(64 * WM * WN) void k_muon_gemm(const MuonMat *mats,
         }
         P += p_step;
         Q += q_step;
+        if (WIDE && --left == 0) {
+            left = K / 32;
+            P = pass == 0 ? Pl : Ph;
+            Q = Qh;
+            ++pass;
+        }
     };
     constexpr int kAhead = (RING - 2) * PANELS * 2 * kLoads;   // copies that may stay out at a wait
 
@@ -429,7 +472,16 @@ __global__ __launch_bounds__(64 * WM * WN) void k_muon_gemm(const MuonMat *mats,
     const auto frag = [&](const _Float16 *p, int row, int kk) {
         return *reinterpret_cast<const half8 *>(p + row * 32 + (((kk * 2 + half) ^ ((row >> 2) & 3)) * 8));
     };
-    const int steps = K / (32 * PANELS);
+    const int steps = (WIDE ? 3 : 1) * (K / (32 * PANELS));
+    // Wide B X on the tiles of deep matrices: the sums of Ph Qh, whose many
+    // roundings at the size of U's strong directions end up in its weak ones, go
+    // to X every kFlush steps (2048^2 of rank 4 plus 1% noise: O 2.5e-5 off
+    // without, 1.4e-5 with).  Smaller tiles would lose their second wave to it
+    // (8 x 1536 x 576: 783 us against 573).
+    constexpr bool kFlushes = WIDE && T == 256 && (MODE == kUpdate || MODE == kOrtho || MODE == kStep);
+    constexpr int kFlush = 1024 / (32 * PANELS);
+    int next_flush = steps / 3 * 2 + kFlush;
+    float scale = ca;   // of the X in F
 #pragma unroll
     for (int s = 0; s < RING - 1; ++s)
         if (s < steps)
@@ -502,6 +554,29 @@ __global__ __launch_bounds__(64 * WM * WN) void k_muon_gemm(const MuonMat *mats,
         }
         asm volatile("" ::: "memory");
         slot = slot + 1 == RING ? 0 : slot + 1;
+        if (kFlushes && k + 1 == next_flush && k + 1 < steps) {
+            float *F = t.F;
+            const int64_t across = t.np >> 5;
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        const int64_t bi = i0 / 32 + wm * TM + i, bj = j0 / 32 + wn * TN + j;
+                        float4v *at = reinterpret_cast<float4v *>(
+                            F + (bi * across + bj) * 1024 + lane * 4 + g * 256);
+                        float4v x = *at;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            x[e] = fmaf(scale, x[e], acc[i][j][4 * g + e] * kUnscale);
+                            acc[i][j][4 * g + e] = 0.f;
+                        }
+                        *at = x;
+                    }
+            scale = 1.f;
+            next_flush += kFlush;
+        }
     }
     if (PAIRED && wave < NW / 2)
         __builtin_amdgcn_s_barrier();   // as many as the second four
@@ -528,46 +603,64 @@ __global__ __launch_bounds__(64 * WM * WN) void k_muon_gemm(const MuonMat *mats,
     for (int i = 0; i < TM; ++i) {
         const int64_t bi = i0 / 32 + wm * TM + i;
         if (MODE == kGram || MODE == kPoly) {
-            half4 x[TN][4];
+            half4 x[TN][4], rest[TN][4];
             if (MODE == kPoly)
 #pragma unroll
                 for (int j = 0; j < TN; ++j)
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
                         const int64_t bj = j0 / 32 + wn * TN + j;
-                        x[j][g] = *reinterpret_cast<const half4 *>(
-                            t.A + (bi * t.mp + bj * 32 + low) * 32 + half * 4 + g * 8);
+                        const int64_t from = (bi * t.mp + bj * 32 + low) * 32 + half * 4 + g * 8;
+                        x[j][g] = *reinterpret_cast<const half4 *>(t.A + from);
+                        if (WIDE)
+                            rest[j][g] = *reinterpret_cast<const half4 *>(t.Al + from);
                     }
-            _Float16 *D = MODE == kGram ? t.A : t.B;
+            _Float16 *D = MODE == kGram ? t.A : t.B, *Dl = MODE == kGram ? t.Al : t.Bl;
 #pragma unroll
             for (int j = 0; j < TN; ++j) {
                 const int64_t bj = j0 / 32 + wn * TN + j;
-                _Float16 *at = D + (bi * t.mp + bj * 32 + low) * 32 + half * 4;
-                _Float16 *mirror = D + (bj * t.mp + bi * 32 + half * 4 + (lane & 3)) * 32 + (low & ~3);
+                const int64_t at = (bi * t.mp + bj * 32 + low) * 32 + half * 4;
+                const int64_t mirror = (bj * t.mp + bi * 32 + half * 4 + (lane & 3)) * 32 + (low & ~3);
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
-                    half4 h;
+                    half4 h, l;
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         float v = acc[i][j][4 * g + k] * kUnscale;
-                        if (MODE == kPoly)
-                            v = fmaf(cc, v, cb * (float)x[j][g][k]);
+                        if (MODE == kPoly) {
+                            const float a = WIDE ? (float)x[j][g][k] + (float)rest[j][g][k] : (float)x[j][g][k];
+                            v = fmaf(cc, v, cb * a);
+                        }
                         h[k] = (_Float16)v;
+                        if (WIDE)
+                            l[k] = low_part(v);
                     }
-                    *reinterpret_cast<half4 *>(at + g * 8) = h;
-                    if (tl.ti != tl.tj)
-                        *reinterpret_cast<half4 *>(mirror + g * 256) = quad_transpose(h);
+                    *reinterpret_cast<half4 *>(D + at + g * 8) = h;
+                    if (WIDE)
+                        *reinterpret_cast<half4 *>(Dl + at + g * 8) = l;
+                    if (tl.ti != tl.tj) {
+                        *reinterpret_cast<half4 *>(D + mirror + g * 256) = quad_transpose(h);
+                        if (WIDE)
+                            *reinterpret_cast<half4 *>(Dl + mirror + g * 256) = quad_transpose(l);
+                    }
                 }
             }
         } else {
             // X is its operand copy (which this tile has just multiplied) plus
-            // the low part
+            // the low part, or with wide products kept as it is: 22 bits add
+            // 1e-5 to the error of a low-rank U there, 32 half of that
             half4 hi[TN][4], lo[TN][4];
+            float4v full[TN][4];
 #pragma unroll
             for (int j = 0; j < TN; ++j)
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
                     const int64_t bj = j0 / 32 + wn * TN + j;
+                    if (WIDE) {
+                        full[j][g] = *reinterpret_cast<const float4v *>(
+                            t.F + (bi * (t.np >> 5) + bj) * 1024 + lane * 4 + g * 256);
+                        continue;
+                    }
                     hi[j][g] = *reinterpret_cast<const half4 *>(
                         t.Y[src] + (bi * t.np + bj * 32 + low) * 32 + half * 4 + g * 8);
                     lo[j][g] = *reinterpret_cast<const half4 *>(
@@ -580,15 +673,18 @@ __global__ __launch_bounds__(64 * WM * WN) void k_muon_gemm(const MuonMat *mats,
                 for (int g = 0; g < 4; ++g)
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        x[j][g][k] = fmaf(ca, (float)hi[j][g][k] + (float)lo[j][g][k],
+                        x[j][g][k] = fmaf(WIDE ? scale : ca, WIDE ? full[j][g][k] : (float)hi[j][g][k] + (float)lo[j][g][k],
                                           acc[i][j][4 * g + k] * kUnscale);
 #pragma unroll
             for (int j = 0; j < TN; ++j) {
                 const int64_t bj = j0 / 32 + wn * TN + j;
                 if (MODE == kUpdate) {
-                    _Float16 *rest = t.L + (bi * (t.np >> 5) + bj) * 1024 + lane * 4;
-                    _Float16 *yt = t.Y[src ^ 1] + (bi * t.np + bj * 32 + low) * 32 + half * 4;
-                    _Float16 *xt = t.X + (bj * t.mp + bi * 32 + half * 4 + (lane & 3)) * 32 + (low & ~3);
+                    const int64_t place = (bi * (t.np >> 5) + bj) * 1024 + lane * 4;
+                    const int64_t y_at = (bi * t.np + bj * 32 + low) * 32 + half * 4;
+                    const int64_t x_at = (bj * t.mp + bi * 32 + half * 4 + (lane & 3)) * 32 + (low & ~3);
+                    _Float16 *rest = t.L + place, *yt = t.Y[src ^ 1] + y_at, *xt = t.X + x_at;
+                    _Float16 *yl = t.Yl[src ^ 1] + y_at, *xl = t.Xl + x_at;
+                    float *whole = t.F + place;
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
                         half4 h, l;
@@ -597,7 +693,13 @@ __global__ __launch_bounds__(64 * WM * WN) void k_muon_gemm(const MuonMat *mats,
                             h[k] = (_Float16)x[j][g][k];
                             l[k] = low_part(x[j][g][k]);
                         }
-                        *reinterpret_cast<half4 *>(rest + g * 256) = l;
+                        if (WIDE) {
+                            *reinterpret_cast<float4v *>(whole + g * 256) = x[j][g];
+                            *reinterpret_cast<half4 *>(yl + g * 8) = l;
+                            *reinterpret_cast<half4 *>(xl + g * 256) = quad_transpose(l);
+                        } else {
+                            *reinterpret_cast<half4 *>(rest + g * 256) = l;
+                        }
                         *reinterpret_cast<half4 *>(yt + g * 8) = h;
                         *reinterpret_cast<half4 *>(xt + g * 256) = quad_transpose(h);
                     }
@@ -611,6 +713,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_muon_gemm(const MuonMat *mats,
 
 // A = X X^T from the pieces' sums, added in order: a workgroup of four waves
 // per 64 x 64 tile, lanes as in the product.
+template <bool WIDE>
 __global__ __launch_bounds__(256) void k_muon_join(const MuonMat *mats, const MuonTile *tiles,
                                                    const float *parts, int splits)
 {
@@ -629,51 +732,62 @@ __global__ __launch_bounds__(256) void k_muon_join(const MuonMat *mats, const Mu
 #pragma unroll
         for (int g = 0; g < 4; ++g)
             s[g] += *reinterpret_cast<const float4v *>(from + (int64_t)q * 4096 + g * 256);
-    _Float16 *at = t.A + (bi * t.mp + bj * 32 + low) * 32 + half * 4;
-    _Float16 *mirror = t.A + (bj * t.mp + bi * 32 + half * 4 + (lane & 3)) * 32 + (low & ~3);
+    const int64_t at = (bi * t.mp + bj * 32 + low) * 32 + half * 4;
+    const int64_t mirror = (bj * t.mp + bi * 32 + half * 4 + (lane & 3)) * 32 + (low & ~3);
+    _Float16 *A = t.A, *Al = t.Al;
+    const bool both = tl.ti != tl.tj;
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
-        half4 h;
+        half4 h, l;
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < 4; ++k) {
             h[k] = (_Float16)(s[g][k] * kUnscale);
-        *reinterpret_cast<half4 *>(at + g * 8) = h;
-        if (tl.ti != tl.tj)
-            *reinterpret_cast<half4 *>(mirror + g * 256) = quad_transpose(h);
+            if (WIDE)
+                l[k] = low_part(s[g][k] * kUnscale);
+        }
+        *reinterpret_cast<half4 *>(A + at + g * 8) = h;
+        if (WIDE)
+            *reinterpret_cast<half4 *>(Al + at + g * 8) = l;
+        if (both) {
+            *reinterpret_cast<half4 *>(A + mirror + g * 256) = quad_transpose(h);
+            if (WIDE)
+                *reinterpret_cast<half4 *>(Al + mirror + g * 256) = quad_transpose(l);
+        }
     }
 }
 
-template <Mode MODE>
+template <Mode MODE, bool WIDE>
 void product(const MuonTables &t, const MuonUpdate &u, int src, hipStream_t s)
 {
     const int p = MODE == kGram ? 0 : MODE == kPoly ? 1 : 2;
     const uint32_t n = (uint32_t)t.n_tiles[p];
     if (t.tile[p] == 256)
-        k_muon_gemm<256, 2, 4, 1, 4, true, MODE><<<n, 512, 0, s>>>(t.mats, t.tiles[p], src, t.a, t.b, t.c, u, nullptr, 1);
+        k_muon_gemm<256, 2, 4, 1, 4, true, MODE, WIDE><<<n, 512, 0, s>>>(t.mats, t.tiles[p], src, t.a, t.b, t.c, u, nullptr, 1);
     else if (t.tile[p] == 128)
-        k_muon_gemm<128, 2, 2, 1, 3, false, MODE><<<n, 256, 0, s>>>(t.mats, t.tiles[p], src, t.a, t.b, t.c, u, nullptr, 1);
+        k_muon_gemm<128, 2, 2, 1, 3, false, MODE, WIDE><<<n, 256, 0, s>>>(t.mats, t.tiles[p], src, t.a, t.b, t.c, u, nullptr, 1);
     else
-        k_muon_gemm<64, 2, 2, 2, 3, false, MODE><<<n, 256, 0, s>>>(t.mats, t.tiles[p], src, t.a, t.b, t.c, u, nullptr, 1);
+        k_muon_gemm<64, 2, 2, 2, 3, false, MODE, WIDE><<<n, 256, 0, s>>>(t.mats, t.tiles[p], src, t.a, t.b, t.c, u, nullptr, 1);
 }
 
+template <bool WIDE>
 void iterate(const MuonTables &t, const MuonUpdate &u, int ns_steps, hipStream_t s)
 {
     for (int k = 0; k < ns_steps; ++k) {
         const int src = k & 1;
         if (t.splits > 1) {
-            k_muon_gemm<64, 2, 2, 2, 3, false, kGramPart><<<(uint32_t)(t.n_tiles[0] * t.splits), 256, 0, s>>>(
+            k_muon_gemm<64, 2, 2, 2, 3, false, kGramPart, WIDE><<<(uint32_t)(t.n_tiles[0] * t.splits), 256, 0, s>>>(
                 t.mats, t.pieces, src, t.a, t.b, t.c, u, t.parts, t.splits);
-            k_muon_join<<<(uint32_t)t.n_tiles[0], 256, 0, s>>>(t.mats, t.tiles[0], t.parts, t.splits);
+            k_muon_join<WIDE><<<(uint32_t)t.n_tiles[0], 256, 0, s>>>(t.mats, t.tiles[0], t.parts, t.splits);
         } else {
-            product<kGram>(t, u, src, s);
+            product<kGram, WIDE>(t, u, src, s);
         }
-        product<kPoly>(t, u, src, s);
+        product<kPoly, WIDE>(t, u, src, s);
         if (k + 1 < ns_steps)
-            product<kUpdate>(t, u, src, s);
+            product<kUpdate, WIDE>(t, u, src, s);
         else if (u.step)
-            product<kStep>(t, u, src, s);
+            product<kStep, WIDE>(t, u, src, s);
         else
-            product<kOrtho>(t, u, src, s);
+            product<kOrtho, WIDE>(t, u, src, s);
     }
 }
 
@@ -948,7 +1062,7 @@ void small(const MuonTables &t, const MuonUpdate &u, int ns_steps, hipStream_t s
     k_muon_small<BF, STEP><<<(uint32_t)t.n_small, 512, 0, s>>>(t.mats + t.n, u, ns_steps, t.a, t.b, t.c, t.eps);
 }
 
-template <bool BF, bool STEP>
+template <bool BF, bool STEP, bool WIDE>
 void first(const MuonTables &t, const MuonUpdate &u, hipStream_t s)
 {
     k_muon_momentum<BF, STEP><<<(uint32_t)t.n_chunks, 256, 0, s>>>(t.mats, t.chunks, t.partials, u);
@@ -957,8 +1071,18 @@ void first(const MuonTables &t, const MuonUpdate &u, hipStream_t s)
     const bool apart = t.n_part_most > 256;
     if (apart)
         k_muon_norm<<<(uint32_t)t.n, 256, 0, s>>>(t.mats, t.partials, t.inv, t.eps);
-    k_muon_cast<BF, STEP><<<(uint32_t)t.n_cast, 256, 0, s>>>(
+    k_muon_cast<BF, STEP, WIDE><<<(uint32_t)t.n_cast, 256, 0, s>>>(
         t.mats, t.cast, apart ? t.inv : nullptr, t.partials, t.eps, u);
+}
+
+template <bool WIDE>
+void tiled(const MuonTables &t, const MuonUpdate &u, int ns_steps, hipStream_t s)
+{
+    if (t.grad_bf16)
+        u.step ? first<true, true, WIDE>(t, u, s) : first<true, false, WIDE>(t, u, s);
+    else
+        u.step ? first<false, true, WIDE>(t, u, s) : first<false, false, WIDE>(t, u, s);
+    iterate<WIDE>(t, u, ns_steps, s);
 }
 
 }  // namespace
@@ -973,11 +1097,7 @@ hipError_t launch_muon(const MuonTables &t, const MuonUpdate &u, int ns_steps, h
     }
     if (t.n == 0)
         return hipGetLastError();
-    if (t.grad_bf16)
-        u.step ? first<true, true>(t, u, s) : first<true, false>(t, u, s);
-    else
-        u.step ? first<false, true>(t, u, s) : first<false, false>(t, u, s);
-    iterate(t, u, ns_steps, s);
+    t.wide ? tiled<true>(t, u, ns_steps, s) : tiled<false>(t, u, ns_steps, s);
     return hipGetLastError();
 }
 

@@ -36,7 +36,8 @@ inline bool muon_small(int64_t mp, int64_t np)
 // 24 x 2048^2 7936 / 6364 / 5551; single products of 2 x 2048 x 8192
 // (128 / 256) 112 / 157, 34 / 53 and 207 / 181, of 4 x 2048^2 62 / 62, 63 / 65
 // and 113 / 87, of 4096 x 11008 245 / 250, 99 / 104 and 472 / 401.
-inline int pick_tile(int product, int32_t n, const int64_t *rows, const int64_t *cols)
+// passes: how often each panel is read, 3 for the wide products.
+inline int pick_tile(int product, int32_t n, const int64_t *rows, const int64_t *cols, int passes = 1)
 {
     static const struct {
         int side;
@@ -52,7 +53,7 @@ inline int pick_tile(int product, int32_t n, const int64_t *rows, const int64_t 
             const double q = m / c.side;
             const double t = product == 2 ? q * (w / c.side) : q * (q + 1) / 2;
             tiles += t;
-            work += t * (product == 0 ? w : m) / 32;
+            work += t * (product == 0 ? w : m) / 32 * passes;
         }
         if (n == 0)
             break;

@@ -179,7 +179,7 @@ size_t reserve(size_t &at, size_t count)
     return here;
 }
 
-z1_status muon_create(z1_muon **out, const z1_muon_bind *b, z1_stream stream)
+z1_status muon_create(z1_muon **out, const z1_muon_bind *b, bool wide, z1_stream stream)
 {
     const int32_t n = b->n;
     const int dev = current_device();
@@ -192,6 +192,7 @@ z1_status muon_create(z1_muon **out, const z1_muon_bind *b, z1_stream stream)
     m->ns_steps = b->ns_steps;
     MuonTables &t = m->t;
     t.grad_bf16 = b->grad_dtype == Z1_BF16;
+    t.wide = wide;
     t.a = (float)b->a;
     t.b = (float)b->b;
     t.c = (float)b->c;
@@ -200,7 +201,7 @@ z1_status muon_create(z1_muon **out, const z1_muon_bind *b, z1_stream stream)
     std::vector<int32_t> order, few;
     std::vector<int64_t> rows, cols;
     for (int32_t i = 0; i < n; ++i) {
-        if (z1::ops::muon_small(pad_to(std::min(b->rows[i], b->cols[i]), 32),
+        if (!wide && z1::ops::muon_small(pad_to(std::min(b->rows[i], b->cols[i]), 32),
                                 pad_to(std::max(b->rows[i], b->cols[i]), 32))) {
             few.push_back(i);
         } else {
@@ -214,7 +215,7 @@ z1_status muon_create(z1_muon **out, const z1_muon_bind *b, z1_stream stream)
     order.insert(order.end(), few.begin(), few.end());
     int32_t whole = 64;   // sides are padded to whole tiles of every product
     for (int p = 0; p < 3; ++p) {
-        t.tile[p] = pick_tile(p, t.n, rows.data(), cols.data());
+        t.tile[p] = pick_tile(p, t.n, rows.data(), cols.data(), wide ? 3 : 1);
         whole = std::max(whole, t.tile[p]);
     }
 
@@ -301,16 +302,15 @@ z1_status muon_create(z1_muon **out, const z1_muon_bind *b, z1_stream stream)
     const size_t o_sums = reserve<float>(bytes, pieces.size() * 64 * 64);
     const size_t o_part = reserve<double>(bytes, chunks.size());
     const size_t o_inv = reserve<double>(bytes, mats.size());
+    // each matrix's operands: X, Y, Y, A, B, then L, or the five's remainders
+    // and F
+    const size_t n_bufs = wide ? 11 : 6;
     std::vector<size_t> offs;
     for (int32_t at = 0; at < t.n; ++at) {
         const MuonMat &q = mats[(size_t)at];
         const size_t mn = (size_t)q.mp * (size_t)q.np, mm = (size_t)q.mp * (size_t)q.mp;
-        offs.push_back(reserve<_Float16>(bytes, mn));
-        offs.push_back(reserve<_Float16>(bytes, mn));
-        offs.push_back(reserve<_Float16>(bytes, mn));
-        offs.push_back(reserve<_Float16>(bytes, mn));
-        offs.push_back(reserve<_Float16>(bytes, mm));
-        offs.push_back(reserve<_Float16>(bytes, mm));
+        for (size_t k = 0; k < n_bufs; ++k)
+            offs.push_back(reserve<_Float16>(bytes, k == 10 ? 2 * mn : k % 5 < 3 ? mn : mm));
     }
     if (hipMalloc(&m->block, bytes) != hipSuccess) {
         (void)hipGetLastError();
@@ -320,13 +320,22 @@ z1_status muon_create(z1_muon **out, const z1_muon_bind *b, z1_stream stream)
     char *base = static_cast<char *>(m->block);
     for (size_t i = 0; i < (size_t)t.n; ++i) {
         MuonMat &q = mats[i];
-        const size_t *o = &offs[6 * i];
-        q.X = reinterpret_cast<_Float16 *>(base + o[0]);
-        q.Y[0] = reinterpret_cast<_Float16 *>(base + o[1]);
-        q.Y[1] = reinterpret_cast<_Float16 *>(base + o[2]);
-        q.L = reinterpret_cast<_Float16 *>(base + o[3]);
-        q.A = reinterpret_cast<_Float16 *>(base + o[4]);
-        q.B = reinterpret_cast<_Float16 *>(base + o[5]);
+        const auto buf = [&](size_t k) { return reinterpret_cast<_Float16 *>(base + offs[n_bufs * i + k]); };
+        q.X = buf(0);
+        q.Y[0] = buf(1);
+        q.Y[1] = buf(2);
+        q.A = buf(3);
+        q.B = buf(4);
+        if (wide) {
+            q.Xl = buf(5);
+            q.Yl[0] = buf(6);
+            q.Yl[1] = buf(7);
+            q.Al = buf(8);
+            q.Bl = buf(9);
+            q.F = reinterpret_cast<float *>(buf(10));
+        } else {
+            q.L = buf(5);
+        }
     }
     t.mats = reinterpret_cast<MuonMat *>(base + o_mats);
     t.chunks = reinterpret_cast<MuonChunk *>(base + o_chunks);
@@ -358,13 +367,7 @@ z1_status muon_create(z1_muon **out, const z1_muon_bind *b, z1_stream stream)
     return Z1_OK;
 }
 
-}  // namespace
-
-extern "C" {
-
-int32_t z1_ops_abi_version(void) { return Z1_OPS_ABI_VERSION; }
-
-z1_status z1_muon_create(z1_muon **out, const z1_muon_bind *b, z1_stream stream)
+z1_status muon_checked(z1_muon **out, const z1_muon_bind *b, bool wide, z1_stream stream)
 {
     if (out)
         *out = nullptr;
@@ -404,7 +407,23 @@ z1_status z1_muon_create(z1_muon **out, const z1_muon_bind *b, z1_stream stream)
             }
         }
     }
-    return no_throw([&] { return muon_create(out, b, stream); });
+    return no_throw([&] { return muon_create(out, b, wide, stream); });
+}
+
+}  // namespace
+
+extern "C" {
+
+int32_t z1_ops_abi_version(void) { return Z1_OPS_ABI_VERSION; }
+
+z1_status z1_muon_create(z1_muon **out, const z1_muon_bind *b, z1_stream stream)
+{
+    return muon_checked(out, b, false, stream);
+}
+
+z1_status z1_muon_create_wide(z1_muon **out, const z1_muon_bind *b, z1_stream stream)
+{
+    return muon_checked(out, b, true, stream);
 }
 
 z1_status z1_muon_destroy(z1_muon *m)

@@ -87,6 +87,10 @@ struct MuonMat {
     _Float16 *Y[2];         // np rows, mp deep: of X^T, one being read and one written
     _Float16 *A, *B;        // mp rows, mp deep
     _Float16 *L;            // what the operand copy of X leaves of it (see carry_at)
+    // wide products: what each operand leaves of its value, laid out as it, and
+    // X itself in fp32, laid out as L (which they do without)
+    _Float16 *Xl, *Yl[2], *Al, *Bl;
+    float *F;
     double lr_scale, wd_scale;
 };
 
@@ -119,6 +123,7 @@ struct MuonTables {
     int32_t n;                 // matrices of the tiled path: mats[0 .. n - 1]
     int32_t n_small;           // those one workgroup takes whole: the n_small after them
     int32_t grad_bf16;
+    int32_t wide;              // products of 22-bit operands
     float a, b, c;
     double eps;
 };

@@ -54,14 +54,14 @@ def rms_lr_scale(shapes: Sequence[Sequence[int]], rms: float = 0.2) -> List[floa
 class MuonStep:
     """Buffers and handles of the matrices one rank owns.  master, momentum and
     acc are fp32 arenas in the plan's order, weights and grads[k] bf16 tensors
-    of the given shapes."""
+    of the given shapes.  wide: as in ops.z1_muon_create."""
 
     def __init__(self, shapes: Sequence[Sequence[int]], n_micro: int, device="cuda",
                  weights: Optional[List[torch.Tensor]] = None,
                  grads: Optional[List[List[torch.Tensor]]] = None,
                  lr_scale: Optional[Sequence[float]] = None,
                  wd_scale: Optional[Sequence[float]] = None, ns_steps: int = 5,
-                 coeffs=ops.MUON_COEFFS, eps: float = 1e-7):
+                 coeffs=ops.MUON_COEFFS, eps: float = 1e-7, wide: bool = False):
         self.shapes = [tuple(int(x) for x in s) for s in shapes]
         self.numel = [m * n for m, n in self.shapes]
         self.n_micro = n_micro
@@ -84,7 +84,7 @@ class MuonStep:
                                        momentum=self.views(self.momentum),
                                        master=self.views(self.master), weights=self.weights,
                                        lr_scale=lr_scale, wd_scale=wd_scale, ns_steps=ns_steps,
-                                       coeffs=coeffs, eps=eps)
+                                       coeffs=coeffs, eps=eps, wide=wide)
 
     def views(self, arena: torch.Tensor) -> List[torch.Tensor]:
         """The matrices of an arena."""

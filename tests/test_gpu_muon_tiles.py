@@ -228,3 +228,119 @@ def test_a_low_rank_gradient_on_large_tiles():
     st(lr=1.0, momentum=0.0)
     check(-st.master[0], orthogonal(st.grads[0]), TOL, by_block=False)
     st.muon.close()
+
+
+def wide_tol(shape):
+    """Wide products: the operands keep 22 bits (2^-22 off, and as much again
+    for the product left out), and 3 K / 16 products are added in fp32 (2^-24
+    each, in squares).  The amplification over five steps is that counted in
+    test_gpu_muon.py, 26 / sqrt(3) in squares and 5 * 21 in a plain sum."""
+    off = math.sqrt(2.0) * 2.0 ** -22 + math.sqrt(3 * max(max(shape), 64) / 16) * 2.0 ** -24
+    return (26 / math.sqrt(3) if min(shape) >= 16 else 105) * off
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=str)
+@pytest.mark.parametrize("shapes", LARGE + TILED + SMALL + [[(2, 3), (96, 200), (5, 1)]], ids=str)
+def test_wide_products(shapes, dtype):
+    """A step from a zero master is -O itself; the orthogonalisation is that,
+    rounded, and repeats its bits."""
+    st = Step(shapes, dtype, zero=True, wide=True)
+    st(lr=1.0, momentum=0.0)
+    for s, g, p in zip(shapes, st.grads, st.master):
+        check(-p, orthogonal(g), wide_tol(s), by_block=min(s) >= 16)
+    st.muon.close()
+    out = [torch.full(s, float("nan"), device="cuda", dtype=torch.bfloat16) for s in shapes]
+    m = O.z1_muon_create(shapes, st.grads, ortho=out, wide=True)
+    for again in range(2):
+        O.z1_muon_orthogonalize(m)
+        torch.cuda.synchronize()
+        for o, p in zip(out, st.master):
+            assert torch.equal(o, (-p).to(torch.bfloat16))
+            o.fill_(7.0)
+    m.close()
+
+
+@pytest.mark.parametrize("shapes", [[(64, 96)], [(300, 1030)], [(2048, 2048)] * 4, [(4001, 9003)]], ids=str)
+def test_wide_low_rank(shapes):
+    st = Step(shapes, zero=True, spectrum="lowrank", wide=True)
+    st(lr=1.0, momentum=0.0)
+    for s, g, p in zip(shapes, st.grads, st.master):
+        check(-p, orthogonal(g), wide_tol(s), by_block=False)
+    st.muon.close()
+
+
+@pytest.mark.parametrize("coeffs,steps", [((1.5, -0.5, 0.0), 12), (O.MUON_COEFFS, 1), (O.MUON_COEFFS, 2)], ids=str)
+@pytest.mark.parametrize("shift", [0, 1])
+def test_wide_steps_and_buffers(coeffs, steps, shift):
+    shapes = TILED[4] + [(64, 96)]
+    st = Step(shapes, torch.float32, shift, zero=True, wide=True, coeffs=coeffs, ns_steps=steps)
+    st(lr=1.0, momentum=0.0)
+    for s, g, p in zip(shapes, st.grads, st.master):
+        check(-p, orthogonal(g, steps, coeffs), math.sqrt(max(1.0, steps / 5)) * wide_tol(s))
+    st.muon.close()
+
+
+@pytest.mark.parametrize("shapes", [TILED[4], [(170, 4100)] * 4], ids=str)
+def test_wide_zero_and_nonfinite_stay_in_their_matrix(shapes):
+    st = Step(shapes, zero=True, wide=True)
+    clean = [g.clone() for g in st.grads]
+    st.grads[0].zero_()
+    st.grads[1][3, 5] = float("nan")
+    st.grads[2][0, 0] = float("inf")
+    O.z1_muon_step(st.muon, lr=1.0, momentum=0.0)
+    torch.cuda.synchronize()
+    assert (st.master[0] == 0).all() and torch.isnan(st.master[1]).all() and torch.isnan(st.master[2]).all()
+    check(-st.master[3], orthogonal(st.grads[3]), wide_tol(shapes[3]))
+    for g, x, mo, p in zip(st.grads, clean, st.momentum, st.master):
+        g.copy_(x)
+        mo.zero_()
+        p.zero_()
+    st(lr=1.0, momentum=0.0)
+    for s, g, p in zip(shapes, st.grads, st.master):
+        check(-p, orthogonal(g), wide_tol(s))
+    st.muon.close()
+
+
+def test_wide_in_a_graph_and_on_another_stream():
+    shapes = [(300, 200), (128, 512), (170, 4100)]
+    gs = [matrix(s, i) for i, s in enumerate(shapes)]
+    out = [torch.zeros(s, device="cuda", dtype=torch.bfloat16) for s in shapes]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    m = O.z1_muon_create(shapes, gs, ortho=out, wide=True, stream=s)
+    O.z1_muon_orthogonalize(m, stream=s)
+    s.synchronize()
+    first = [o.clone() for o in out]
+    for g, o in zip(gs, out):
+        check(o, orthogonal(g), HALF + 1e-4)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        O.z1_muon_orthogonalize(m)
+    for k in range(4):
+        for o in out:
+            o.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(first, out)), k
+        O.z1_muon_orthogonalize(m)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(first, out)), k
+    m.close()
+
+
+def test_wide_through_muon_step_and_an_empty_list():
+    from mixed_precision_zero_amd.muon import MuonStep
+    shapes = [(64, 96), (300, 130)]
+    st = MuonStep(shapes, 1, wide=True)
+    g = torch.Generator(device="cuda").manual_seed(0)
+    for t in st.grads[0]:
+        t.copy_(torch.randn(t.shape, generator=g, device="cuda") * 1e-3)
+    st.step(lr=1.0, momentum=0.0)
+    torch.cuda.synchronize()
+    for s, t, p in zip(shapes, st.grads[0], st.views(st.master)):
+        check(-p, orthogonal(t), wide_tol(s))
+    st.close()
+    m = O.z1_muon_create([], [], ortho=[], wide=True)
+    O.z1_muon_orthogonalize(m)
+    m.close()

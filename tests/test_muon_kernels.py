@@ -19,9 +19,10 @@ int main(int argc, char **argv)
 {
     std::vector<int64_t> rows, cols;
     int n_small = 0;
-    for (int i = 1; i + 1 < argc; i += 2) {
+    const int passes = atoi(argv[1]);   // 3: wide products, which one workgroup does not take
+    for (int i = 2; i + 1 < argc; i += 2) {
         const int64_t r = atoll(argv[i]), c = atoll(argv[i + 1]);
-        if (muon_small(pad_to(std::min(r, c), 32), pad_to(std::max(r, c), 32))) {
+        if (passes == 1 && muon_small(pad_to(std::min(r, c), 32), pad_to(std::max(r, c), 32))) {
             ++n_small;
         } else {
             rows.push_back(r);
@@ -32,7 +33,7 @@ int main(int argc, char **argv)
     int tile[3];
     int64_t whole = 64, tiles = 0, panels = INT64_MAX;
     for (int p = 0; p < 3; ++p) {
-        tile[p] = pick_tile(p, n, rows.data(), cols.data());
+        tile[p] = pick_tile(p, n, rows.data(), cols.data(), passes);
         whole = std::max<int64_t>(whole, tile[p]);
     }
     for (int i = 0; i < n; ++i) {
@@ -56,8 +57,8 @@ def kernels_of(tmp_path_factory):
                     os.path.join(ROOT, "mixed_precision_zero_amd", "csrc"), str(at / "t.cpp"), "-o", str(at / "t")],
                    check=True)
 
-    def ask(shapes):
-        out = subprocess.run([str(at / "t")] + [str(x) for s in shapes for x in s], capture_output=True, text=True,
+    def ask(shapes, passes=1):
+        out = subprocess.run([str(at / "t"), str(passes)] + [str(x) for s in shapes for x in s], capture_output=True, text=True,
                              check=True).stdout.split()
         small, a, b, c, splits = map(int, out)
         return small, (a, b, c), splits
@@ -66,11 +67,12 @@ def kernels_of(tmp_path_factory):
 
 
 def test_the_large_lists_reach_every_tile_side_of_every_product(kernels_of):
-    sides = [kernels_of(s)[1] for s in LARGE]
-    for product in range(3):
-        assert {t[product] for t in sides} == {64, 128, 256}, (product, sides)
-    # one of them on 256 throughout, wide and tall
-    assert sides[-2] == sides[-1] == (256, 256, 256)
+    for passes in (1, 3):
+        sides = [kernels_of(s, passes)[1] for s in LARGE]
+        for product in range(3):
+            assert {t[product] for t in sides} == {64, 128, 256}, (product, sides)
+        # one of them on 256 throughout, wide and tall
+        assert sides[-2] == sides[-1] == (256, 256, 256)
     assert all(kernels_of(s)[0] == 0 for s in LARGE)
 
 
@@ -78,7 +80,9 @@ def test_the_tiled_lists_are_tiled_and_the_small_ones_are_not(kernels_of):
     for s in TILED:
         small, tiles, _ = kernels_of(s)
         assert small == 0 and tiles[0] == 64, s
-    assert [kernels_of(s)[2] > 1 for s in TILED[-2:]] == [True, True]
+    for passes in (1, 3):
+        assert [kernels_of(s, passes)[2] > 1 for s in TILED[-2:]] == [True, True]
+        assert kernels_of([(1, 300)], passes)[1] == (64, 64, 64)
     for s in SMALL:
         assert kernels_of(s)[0] == len(s), s
 

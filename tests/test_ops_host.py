@@ -327,3 +327,16 @@ def test_muon_holds_the_memory_it_is_bound_to(monkeypatch):
     assert all(r() is not None for r in alive) and len(alive) == 10
     m.close()
     assert all(r() is None for r in alive)
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(n=-1), B.Z1_EINVAL), (dict(rows1=0), B.Z1_EINVAL), (dict(ns_steps=0), B.Z1_EINVAL), (dict(reserved=1), B.Z1_EINVAL),
+    (dict(master=None), B.Z1_EINVAL), (dict(a=4.0, b=0.0, c=0.0), B.Z1_EINVAL), (dict(at_grad=0), B.Z1_EINVAL),
+    (dict(at_weights=0x40001), B.Z1_EALIGN)])
+def test_wide_muon_create_refuses_the_same(over, status):
+    b, keep = muon_bind(**over)
+    h = ctypes.c_void_p(1)
+    assert B.lib.z1_muon_create_wide(ctypes.byref(h), ctypes.byref(b), None) == status
+    assert h.value is None
+    assert B.lib.z1_muon_create_wide(None, ctypes.byref(b), None) == B.Z1_EINVAL
+    assert B.lib.z1_muon_create_wide(ctypes.byref(h), None, None) == B.Z1_EINVAL
