@@ -24,7 +24,7 @@
  * call can be captured into a HIP graph; its scalar arguments are baked in.
  *
  * Target and token ids live on the device, so the host cannot check their
- * values: an id below zero marks an empty position (nothing is read for it,
+ * values: an id below zero marks an empty position (nothing of its row counts,
  * its outputs are zero), and an id of vocab or more gives NaN in its outputs
  * (and is skipped by z1_embed_grad); neither makes the kernels read or write
  * outside the buffers.

@@ -9,7 +9,10 @@
 // the running sum of the current id in registers.  An id whose run lies
 // inside one chunk is written at once; a run that crosses chunks leaves one
 // partial row per chunk, and the join adds those in order.  Chunks of equal
-// length keep the work even however often the commonest id occurs.
+// length keep the sums' work even however often the commonest id occurs; the
+// join's is not, for one workgroup adds a run's partial rows, four at a time
+// (65536 equal ids: 252 us instead of 210 at 2048 columns, 348 instead of 66 at
+// 64, where chunks are of 16).
 //
 // Lanes are laid over (chunk, 16-byte vector of the row) pairs in one flat
 // order, so that rows of any length fill whole waves.
