@@ -1,0 +1,235 @@
+// z1_layers_internal.h -- what the host code of the layers (z1_layers_api.hip)
+// and their kernels (z1_linear.hip, z1_layers.hip) share.  Not installed.
+#pragma once
+
+#include "z1_layers.h"
+#include "z1_ops_internal.h"
+
+namespace z1 {
+namespace ops {
+
+// z1_drop as the kernels take it; rng null: no dropout.
+struct Drop {
+    const uint64_t *rng;
+    uint64_t offset;
+    uint32_t threshold;   // 0 .. 65536
+    float scale;
+};
+
+// The same with the device's seed and offset read.
+struct DropKey {
+    uint32_t seed[2], offset[2], threshold;
+    float scale;
+    bool on;
+};
+
+__device__ __forceinline__ DropKey drop_key(const Drop &d)
+{
+    DropKey k{};
+    k.on = d.rng != nullptr;
+    if (k.on) {
+        const uint64_t seed = d.rng[0], offset = d.rng[1] + d.offset;
+        k.seed[0] = (uint32_t)seed;
+        k.seed[1] = (uint32_t)(seed >> 32);
+        k.offset[0] = (uint32_t)offset;
+        k.offset[1] = (uint32_t)(offset >> 32);
+        k.threshold = d.threshold;
+        k.scale = d.scale;
+    }
+    return k;
+}
+
+// Philox4x32-10 (Salmon, Moraes, Dror, Shaw 2011): the four words of counter
+// (block, row, offset).  The key schedule is the same for the whole launch and
+// stays in scalar registers; a round is two 32 x 32 bit multiplies.
+__device__ __forceinline__ void philox(const DropKey &k, uint32_t block, uint32_t row, uint32_t (&w)[4])
+{
+    uint32_t a = block, b = row, c = k.offset[0], d = k.offset[1], k0 = k.seed[0], k1 = k.seed[1];
+#pragma unroll
+    for (int i = 0; i < 10; ++i) {
+        const uint64_t p = (uint64_t)a * 0xD2511F53u, q = (uint64_t)c * 0xCD9E8D57u;
+        a = (uint32_t)(q >> 32) ^ b ^ k0;
+        b = (uint32_t)q;
+        c = (uint32_t)(p >> 32) ^ d ^ k1;
+        d = (uint32_t)p;
+        k0 += 0x9E3779B9u;
+        k1 += 0xBB67AE85u;
+    }
+    w[0] = a;
+    w[1] = b;
+    w[2] = c;
+    w[3] = d;
+}
+
+// Eight elements (row, 8 block ..) after dropout.
+__device__ __forceinline__ void drop8(const DropKey &k, uint32_t block, uint32_t row, float (&v)[8])
+{
+    uint32_t w[4];
+    philox(k, block, row, w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const uint32_t u = j & 1 ? w[j >> 1] >> 16 : w[j >> 1] & 0xffffu;
+        v[j] = u >= k.threshold ? v[j] * k.scale : 0.f;
+    }
+}
+
+// Eight elements of type T at any alignment of T, in as few accesses as that
+// takes (the hardware takes vector accesses at any address).
+template <int ALIGN>
+struct Words {
+    typedef uint32_t four __attribute__((ext_vector_type(4), aligned(2)));
+};
+template <>
+struct Words<4> {
+    typedef uint32_t four __attribute__((ext_vector_type(4), aligned(4)));
+};
+
+template <typename T>
+struct Eight {
+    typedef typename Words<(int)sizeof(typename T::store)>::four word4;
+    static __device__ __forceinline__ void load(const void *p, float (&v)[8])
+    {
+        union {
+            uint4v raw[sizeof(typename T::store) / 2];
+            typename T::store e[8];
+        } u;
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(typename T::store) / 2; ++i)
+            u.raw[i] = static_cast<const word4 *>(p)[i];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            v[j] = T::up(u.e[j]);
+    }
+    static __device__ __forceinline__ void store(void *p, const float (&v)[8])
+    {
+        union {
+            uint4v raw[sizeof(typename T::store) / 2];
+            typename T::store e[8];
+        } u;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            u.e[j] = T::down(v[j]);
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(typename T::store) / 2; ++i)
+            static_cast<word4 *>(p)[i] = u.raw[i];
+    }
+    // the first n < 8 of them; the others load as zeros
+    static __device__ __forceinline__ void load_some(const void *p, float (&v)[8], int n)
+    {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            v[j] = j < n ? T::up(static_cast<const typename T::store *>(p)[j]) : 0.f;
+    }
+    static __device__ __forceinline__ void store_some(void *p, const float (&v)[8], int n)
+    {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j < n)
+                static_cast<typename T::store *>(p)[j] = T::down(v[j]);
+    }
+};
+
+// act(z) and act'(z).  Written so that they hold at both ends: the sigmoid
+// underflows to 0 for z << 0 and Phi is taken from erfc, which keeps its
+// relative precision there.
+__device__ __forceinline__ float sigmoid(float z) { return __builtin_amdgcn_rcpf(1.f + expf(-z)); }
+__device__ __forceinline__ float gelu_tanh_arg(float z)
+{
+    return 1.5957691216057308f * z * fmaf(0.044715f * z, z, 1.f);   // 2 sqrt(2 / pi)
+}
+
+__device__ __forceinline__ float act_value(int32_t act, float z)
+{
+    switch (act) {
+    case Z1_ACT_RELU: return z < 0.f ? 0.f : z;
+    case Z1_ACT_GELU: return 0.5f * z * erfcf(z * -0.70710678118654752f);
+    case Z1_ACT_GELU_TANH: return z * sigmoid(gelu_tanh_arg(z));
+    case Z1_ACT_SILU: return z * sigmoid(z);
+    case Z1_ACT_RELU2: {
+        const float r = z < 0.f ? 0.f : z;
+        return r * r;
+    }
+    default: return z;
+    }
+}
+
+__device__ __forceinline__ float act_slope(int32_t act, float z)
+{
+    switch (act) {
+    case Z1_ACT_RELU: return z > 0.f ? 1.f : 0.f;
+    case Z1_ACT_GELU:
+        return fmaf(z * 0.39894228040143268f, expf(-0.5f * z * z), 0.5f * erfcf(z * -0.70710678118654752f));
+    case Z1_ACT_GELU_TANH: {
+        const float s = sigmoid(gelu_tanh_arg(z));
+        return fmaf(z * s * (1.f - s), 1.5957691216057308f * fmaf(3.f * 0.044715f * z, z, 1.f), s);
+    }
+    case Z1_ACT_SILU: {
+        const float s = sigmoid(z);
+        return s * fmaf(z, 1.f - s, 1.f);
+    }
+    case Z1_ACT_RELU2: return 2.f * (z < 0.f ? 0.f : z);
+    default: return 1.f;
+    }
+}
+
+// --------------------------------------------------------------------------
+// Products.  C[q][p] = sum_k P(p, k) Q(q, k), p along C's rows' elements.
+// --------------------------------------------------------------------------
+
+// One operand.  Deep: element (i, k) at base + i * ld + k * size ("the depth is
+// contiguous"); else at base + k * ld + i * size.  ld in bytes, a multiple of
+// 16 as base is; the contiguous extent is whole 16-byte chunks.
+struct Operand {
+    const void *base;
+    int64_t ld;
+    int32_t extent;       // of i
+    int32_t depth;        // of k
+};
+
+// What is done with C's elements.  Plain: out = c + add.  Full: z1_linear's
+// epilogue.  Distances in elements.
+struct Epilogue {
+    void *out, *pre;
+    const void *add, *mul, *bias;
+    int64_t ld_out, ld_pre, ld_add, ld_mul;
+    Drop drop;
+    int32_t act;
+};
+
+struct Product {
+    Operand p, q;
+    int32_t P, Q;          // C's row length and rows
+    Epilogue e;
+    float *parts;          // partial sums of `splits` pieces of the depth
+    int32_t splits;        // 1: not split
+    int32_t piece;         // panels a piece takes
+    int32_t tiles_p, tiles_q;
+    int32_t tile;          // side: 64, 128 or 256
+};
+
+enum Form { kForward, kInput, kWeight };   // x W', dz W, dz' x: which operands are deep
+
+hipError_t launch_product(Form form, int32_t dtype, int32_t out_dtype, const Product &g, hipStream_t s);
+
+// Copies rows of `cols` elements to rows of `cols_to`, zeros behind them.
+hipError_t launch_pack(int32_t dtype, const void *from, int64_t ld, void *to, int64_t cols_to, int64_t rows,
+                       int64_t cols, hipStream_t s);
+
+// --------------------------------------------------------------------------
+// Elementwise layers
+// --------------------------------------------------------------------------
+
+hipError_t launch_dropout(const z1_dropout_args &a, const Drop &d, hipStream_t s);
+
+// Rows of a piece of z1_linear_dz: each piece leaves one row of column sums.
+inline int64_t dz_piece(int64_t rows) { return std::max<int64_t>(64, pad_to((rows + 1023) / 1024, 8)); }
+hipError_t launch_linear_dz(const z1_linear_dz_args &a, const Drop &d, float *parts, hipStream_t s);
+
+// Workgroups of z1_qk_norm_rope_grad, each of which leaves a row of sums for
+// either weight.
+int64_t qk_grad_groups(int64_t tokens, int64_t heads);
+hipError_t launch_qk(const z1_qk_args &a, hipStream_t s);
+hipError_t launch_qk_grad(const z1_qk_args &a, float *parts, hipStream_t s);
+
+}  // namespace ops
+}  // namespace z1

@@ -8,9 +8,11 @@
 #include <memory>
 #include <vector>
 
+#include "z1_host.h"
 #include "z1_ops.h"
 #include "z1_ops_internal.h"
 
+using namespace z1::host;
 using z1::ops::MuonChunk;
 using z1::ops::MuonMat;
 using z1::ops::MuonTables;
@@ -28,41 +30,6 @@ struct z1_muon {
 };
 
 namespace {
-
-bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-int current_device()
-{
-    int d = -1;
-    if (hipGetDevice(&d) != hipSuccess) {
-        (void)hipGetLastError();
-        return -1;
-    }
-    return d;
-}
-
-// True when `stream` is a stream of GPU `dev` and that GPU is current.
-bool runs_on(int dev, z1_stream stream)
-{
-    if (dev < 0 || current_device() != dev)
-        return false;
-    const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-    if (!s || s == hipStreamLegacy || s == hipStreamPerThread)
-        return true;
-    hipDevice_t d = -1;
-    if (hipStreamGetDevice(s, &d) != hipSuccess) {
-        (void)hipGetLastError();
-        return false;
-    }
-    return d == dev;
-}
-
-bool is_finite(double x) { return isfinite(x); }
-
-size_t type_size(int32_t dtype) { return dtype == Z1_F32 ? 4 : 2; }
-bool dtype_ok(int32_t t) { return t == Z1_F32 || t == Z1_BF16 || t == Z1_F16; }
-bool itype_ok(int32_t t) { return t == Z1_I64 || t == Z1_I32; }
-size_t itype_size(int32_t t) { return t == Z1_I64 ? 8 : 4; }
 
 // Host allocations are the only operations of a body that can throw; they
 // become Z1_ENOMEM and never cross the C interface.
