@@ -49,6 +49,9 @@ struct Matrix {
     int64_t rows, cols, ld;
 };
 
+// Copied rows are padded to whole groups of eight elements.
+constexpr int64_t kPackCols = 8;
+
 // Whether a product reads the matrix where it lies: 16-byte chunks throughout.
 bool in_place(const Matrix &m, int32_t dtype)
 {
@@ -68,12 +71,12 @@ Plan plan_product(Form form, int32_t dtype, const Matrix &p, const Matrix &q)
     Plan w;
     Product &g = w.g;
     const bool p_deep = form == z1::ops::kForward, q_deep = form != z1::ops::kWeight;
-    const int64_t size = (int64_t)type_size(dtype), chunk = 16 / size;
+    const int64_t size = (int64_t)type_size(dtype);
     const auto operand = [&](const Matrix &m, bool deep, bool &pack, int64_t &at) {
         pack = !in_place(m, dtype);
         int64_t cols = m.cols, ld = m.ld;
         if (pack) {
-            cols = ld = pad_to(cols, chunk);
+            cols = ld = pad_to(cols, kPackCols);
             at = w.bytes;
             w.bytes += pad_to(m.rows * cols * size, 16);
         } else if (m.rows == 1) {
@@ -110,10 +113,9 @@ z1_status run_product(Form form, int32_t dtype, int32_t out_dtype, Plan &w, cons
 {
     Product &g = w.g;
     char *base = static_cast<char *>(workspace);
-    const int64_t chunk = 16 / (int64_t)type_size(dtype);
     const auto pack = [&](const Matrix &m, int64_t at, Operand &o) {
         o.base = base + at;
-        return z1::ops::launch_pack(dtype, m.p, m.ld, base + at, pad_to(m.cols, chunk), m.rows, m.cols, s);
+        return z1::ops::launch_pack(dtype, m.p, m.ld, base + at, pad_to(m.cols, kPackCols), m.rows, m.cols, s);
     };
     hipError_t e = hipSuccess;
     if (w.pack_p)
