@@ -104,17 +104,22 @@ __global__ __launch_bounds__(256) void k_linear_dz(z1_linear_dz_args a, Drop d, 
                 float o[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    o[j] = g[j] * act_value(a.act, z[j]);
+                    o[j] = z[j];
+                act_values(a.act, o);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    o[j] *= g[j];
                 set8<T>(a.dmul, r * a.ld_dmul + c, n, o);
             }
             if (a.mul)
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
                     g[j] *= m[j];
-            if (a.act != Z1_ACT_NONE)
+            with_act(a.act, [&](auto k) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    g[j] *= act_slope(a.act, z[j]);
+                    g[j] *= act_slope<decltype(k)::value>(z[j]);
+            });
             if (a.dz)
                 set8<T>(a.dz, r * a.ld_dz + c, n, g);
 #pragma unroll

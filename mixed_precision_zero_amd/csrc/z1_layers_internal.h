@@ -138,38 +138,65 @@ __device__ __forceinline__ float gelu_tanh_arg(float z)
     return 1.5957691216057308f * z * fmaf(0.044715f * z, z, 1.f);   // 2 sqrt(2 / pi)
 }
 
-__device__ __forceinline__ float act_value(int32_t act, float z)
+template <int ACT>
+__device__ __forceinline__ float act_value(float z)
 {
-    switch (act) {
-    case Z1_ACT_RELU: return z < 0.f ? 0.f : z;
-    case Z1_ACT_GELU: return 0.5f * z * erfcf(z * -0.70710678118654752f);
-    case Z1_ACT_GELU_TANH: return z * sigmoid(gelu_tanh_arg(z));
-    case Z1_ACT_SILU: return z * sigmoid(z);
-    case Z1_ACT_RELU2: {
+    if constexpr (ACT == Z1_ACT_RELU)
+        return z < 0.f ? 0.f : z;
+    if constexpr (ACT == Z1_ACT_GELU)
+        return 0.5f * z * erfcf(z * -0.70710678118654752f);
+    if constexpr (ACT == Z1_ACT_GELU_TANH)
+        return z * sigmoid(gelu_tanh_arg(z));
+    if constexpr (ACT == Z1_ACT_SILU)
+        return z * sigmoid(z);
+    if constexpr (ACT == Z1_ACT_RELU2) {
         const float r = z < 0.f ? 0.f : z;
         return r * r;
     }
-    default: return z;
-    }
+    return z;
 }
 
-__device__ __forceinline__ float act_slope(int32_t act, float z)
+template <int ACT>
+__device__ __forceinline__ float act_slope(float z)
 {
-    switch (act) {
-    case Z1_ACT_RELU: return z > 0.f ? 1.f : 0.f;
-    case Z1_ACT_GELU:
+    if constexpr (ACT == Z1_ACT_RELU)
+        return z > 0.f ? 1.f : 0.f;
+    if constexpr (ACT == Z1_ACT_GELU)
         return fmaf(z * 0.39894228040143268f, expf(-0.5f * z * z), 0.5f * erfcf(z * -0.70710678118654752f));
-    case Z1_ACT_GELU_TANH: {
+    if constexpr (ACT == Z1_ACT_GELU_TANH) {
         const float s = sigmoid(gelu_tanh_arg(z));
         return fmaf(z * s * (1.f - s), 1.5957691216057308f * fmaf(3.f * 0.044715f * z, z, 1.f), s);
     }
-    case Z1_ACT_SILU: {
+    if constexpr (ACT == Z1_ACT_SILU) {
         const float s = sigmoid(z);
         return s * fmaf(z, 1.f - s, 1.f);
     }
-    case Z1_ACT_RELU2: return 2.f * (z < 0.f ? 0.f : z);
-    default: return 1.f;
+    if constexpr (ACT == Z1_ACT_RELU2)
+        return 2.f * (z < 0.f ? 0.f : z);
+    return 1.f;
+}
+
+// f(a constant) for the activation of this number; nothing for none.
+template <typename F>
+__device__ __forceinline__ void with_act(int32_t act, F &&f)
+{
+    switch (act) {
+    case Z1_ACT_RELU: f(std::integral_constant<int, Z1_ACT_RELU>()); break;
+    case Z1_ACT_GELU: f(std::integral_constant<int, Z1_ACT_GELU>()); break;
+    case Z1_ACT_GELU_TANH: f(std::integral_constant<int, Z1_ACT_GELU_TANH>()); break;
+    case Z1_ACT_SILU: f(std::integral_constant<int, Z1_ACT_SILU>()); break;
+    case Z1_ACT_RELU2: f(std::integral_constant<int, Z1_ACT_RELU2>()); break;
+    default: break;
     }
+}
+
+__device__ __forceinline__ void act_values(int32_t act, float (&v)[8])
+{
+    with_act(act, [&](auto a) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            v[j] = act_value<decltype(a)::value>(v[j]);
+    });
 }
 
 // --------------------------------------------------------------------------
@@ -202,7 +229,7 @@ struct Product {
     Epilogue e;
     float *parts;          // partial sums of `splits` pieces of the depth
     int32_t splits;        // 1: not split
-    int32_t piece;         // panels a piece takes
+    int32_t piece;         // bytes of depth a piece takes, whole panels
     int32_t tiles_p, tiles_q;
     int32_t tile;          // side: 64, 128 or 256
 };

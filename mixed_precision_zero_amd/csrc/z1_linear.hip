@@ -16,6 +16,21 @@ namespace {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short short4v __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) void lds_void;
+// LDS as an address space of its own.  The kernels' loops take the ring as two
+// restrict pointers, one that copies write and one that fragments are read from:
+// else the compiler waits for every copy under way before a transposing read.  What
+// orders the two is the kernels' own waits and barriers, each beside a fence that no
+// memory access is moved across.  (The pointers are passed on by value alone, as what
+// a closure holds by reference loses its restrict, and the second one's value is
+// hidden, as a constant argument does too.)
+typedef __attribute__((address_space(3))) char lds_char;
+[[maybe_unused]] __device__ __forceinline__ const lds_char *hidden(const lds_char *p)
+{
+#if defined(__HIP_DEVICE_COMPILE__)
+    asm("" : "+s"(p));
+#endif
+    return p;
+}
 
 // acc += A B for the 16 bytes of depth that a lane holds of either operand: one
 // instruction of depth 16 in 16 bits, four of depth 2 in fp32 (there, the k of
@@ -38,13 +53,13 @@ typedef __attribute__((address_space(3))) void lds_void;
 
 constexpr uint32_t kRange = 0x7ffffff0u, kOutside = 0x80000000u;
 
-// One operand's share of a panel (64 bytes of depth: 32 or 16 elements) in LDS,
-// TILE * 64 bytes, copied there directly, 1 KiB a wave and instruction; and the
-// fragments of 32 indexes x 16 bytes of depth read from it.
+// One operand's share of a panel (DB bytes of depth, 64 or 128) in LDS, TILE * DB
+// bytes, copied there directly, 1 KiB a wave and instruction; and the fragments of 32
+// indexes x 32 bytes of depth (16 a lane) read from it.
 //
-// Deep operands: a row of 64 bytes for each index.  Four rows span the 64 banks;
-// the 16-byte chunks of row r sit permuted by (r / 4) mod 4, so that the lanes
-// of a fragment read that share a cycle touch all banks once.
+// Deep operands: a row of DB bytes for each index, its 16-byte chunks permuted by the
+// row's number, so that the 16 rows that share a cycle of a fragment read touch all 64
+// banks once: four rows of 64 bytes span the banks, or two of 128.
 //
 // The others: a row for each k, the tile's indexes along it.  In 16 bits the
 // fragments are read with the transposing LDS read: 16 lanes take 16 indexes x
@@ -58,14 +73,17 @@ constexpr uint32_t kRange = 0x7ffffff0u, kOutside = 0x80000000u;
 // the contiguous extent) get an offset outside the descriptor's range and
 // arrive as zeros; rows of a deep operand behind its extent repeat the last one
 // and end up in rows or columns of C that nobody writes.
-template <typename E, bool DEEP, int TILE, int NW>
+template <typename E, bool DEEP, int TILE, int NW, int DB>
 struct Side {
     static constexpr int kSize = (int)sizeof(typename E::store);
-    static constexpr int kPanel = 64 / kSize;             // depth of a panel
-    static constexpr int kLoads = TILE / 16 / NW;         // copies per wave and panel
+    static constexpr int kPanel = DB / kSize;             // depth of a panel
+    static constexpr int kParts = DB / 32;                // fragments along it
+    static constexpr int kBytes = TILE * DB;              // of a panel's share
+    static constexpr int kLoads = kBytes / 1024 / NW;     // copies per wave and panel
+    static constexpr int kReads = (DEEP || kSize == 4) ? (DEEP ? 1 : 4) : 2;   // LDS reads of a fragment
     static constexpr int kRow = TILE * kSize;             // bytes of a row in LDS, if not deep
-    static constexpr int kChunks = kRow / 16;
-    static_assert(kLoads >= 1 && kChunks >= 8, "tile");
+    static constexpr int kChunks = DEEP ? DB / 16 : kRow / 16;   // of a row
+    static_assert(kLoads >= 1 && (DEEP || kChunks >= 8) && (DB == 64 || DB == 128), "tile");
 
     const char *base;        // of the next panel
     int64_t step;
@@ -73,11 +91,14 @@ struct Side {
     uint32_t at[kLoads];     // offsets of this lane's copies
     int32_t limit[kLoads];   // copied while limit < left
 
-    static __device__ __forceinline__ int turn(int k)     // what row k's chunks are xored with
+    // what the chunks of row r are xored with
+    static __device__ __forceinline__ int turn(int r)
     {
+        if (DEEP)
+            return DB == 64 ? (r >> 2) & 3 : (r >> 1) & 7;
         if (kSize == 4)
-            return ((k >> 2) & 1) << 3;
-        return kChunks >= 16 ? (k & 3) << 2 : ((k >> 1) & 1) << 2;
+            return ((r >> 2) & 1) << 3;
+        return kChunks >= 16 ? (r & 3) << 2 : ((r >> 1) & 1) << 2;
     }
 
     __device__ __forceinline__ void start(const Operand &o, int32_t tile, int32_t panel, int wave, int lane)
@@ -85,9 +106,9 @@ struct Side {
         const int32_t i0 = tile * TILE;
         base = static_cast<const char *>(o.base);
         if (DEEP) {
-            base += (int64_t)i0 * o.ld + (int64_t)panel * 64;
-            step = 64;
-            left = o.depth * kSize - panel * 64;
+            base += (int64_t)i0 * o.ld + (int64_t)panel * DB;
+            step = DB;
+            left = o.depth * kSize - panel * DB;
         } else {
             base += (int64_t)panel * kPanel * o.ld + (int64_t)i0 * kSize;
             step = kPanel * o.ld;
@@ -96,29 +117,32 @@ struct Side {
 #pragma unroll
         for (int q = 0; q < kLoads; ++q) {
             const int c = (wave * kLoads + q) * 64 + lane;
+            const int row = c / kChunks, chunk = (c % kChunks) ^ turn(row);
             if (DEEP) {
-                const int row = c >> 2, chunk = (c & 3) ^ ((row >> 2) & 3);
                 at[q] = (uint32_t)min(row, o.extent - 1 - i0) * (uint32_t)o.ld + chunk * 16;
                 limit[q] = chunk * 16;
             } else {
-                const int k = c / kChunks, chunk = (c % kChunks) ^ turn(k);
-                at[q] = (uint32_t)k * (uint32_t)o.ld + chunk * 16;
+                at[q] = (uint32_t)row * (uint32_t)o.ld + chunk * 16;
                 // behind the row's end: never copied
-                limit[q] = (i0 * (int64_t)kSize + chunk * 16 < (int64_t)o.extent * kSize) ? k : INT32_MAX;
+                limit[q] = (i0 * (int64_t)kSize + chunk * 16 < (int64_t)o.extent * kSize) ? row : INT32_MAX;
             }
         }
     }
 
-    // Copies the next panel to `to` in LDS.
-    __device__ __forceinline__ void load(char *to, int wave)
+    // Copies FROM .. TO - 1 of the wave's share of the next panel; the last one
+    // goes on to the panel behind it.
+    template <int FROM = 0, int TO = kLoads>
+    __device__ __forceinline__ void load(lds_char *to, int wave)
     {
         const auto r = __builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(base), 0, kRange, 0x00020000);
 #pragma unroll
-        for (int q = 0; q < kLoads; ++q)
+        for (int q = FROM; q < TO; ++q)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)(to + (wave * kLoads + q) * 1024), 16,
                                                      limit[q] < left ? at[q] : kOutside, 0, 0, 0);
-        base += step;
-        left -= DEEP ? 64 : kPanel;
+        if (TO == kLoads) {
+            base += step;
+            left -= DEEP ? DB : kPanel;
+        }
     }
 
     // Where fragments of the 32 indexes from i0 are read, for frag().
@@ -126,7 +150,7 @@ struct Side {
     {
         const int half = lane >> 5, low = lane & 31;
         if (DEEP)
-            return (i0 + low) * 64 + ((half ^ ((low >> 2) & 3)) * 16);
+            return (i0 + low) * DB + ((half ^ turn(low)) * 16);
         if (kSize == 4) {
             const int k = 4 * half, col = i0 + low;
             return k * kRow + (((col >> 2) ^ turn(k)) << 4) + (col & 3) * 4;
@@ -135,16 +159,16 @@ struct Side {
         return k * kRow + (((col >> 3) ^ turn(k)) << 4) + (col & 7) * 2;
     }
 
-    // The fragment of half kk of the panel's depth.
-    static __device__ __forceinline__ uint4v frag(const char *lds, int place, int kk)
+    // The fragment of part kk of the panel's depth.
+    static __device__ __forceinline__ uint4v frag(const lds_char *lds, int place, int kk)
     {
         if (DEEP)
-            return *reinterpret_cast<const uint4v *>(lds + (place ^ (kk * 32)));
+            return *(const __attribute__((address_space(3))) uint4v *)(lds + (place ^ (kk * 32)));
         if (kSize == 4) {
             uint4v v;
 #pragma unroll
             for (int s = 0; s < 4; ++s)
-                v[s] = *reinterpret_cast<const uint32_t *>(lds + place + (8 * kk + s) * kRow);
+                v[s] = *(const __attribute__((address_space(3))) uint32_t *)(lds + place + (8 * kk + s) * kRow);
             return v;
         }
         union {
@@ -230,10 +254,7 @@ struct FullOut {
         }
         if (e.pre)
             set(e.pre, row * e.ld_pre + col, n, v);
-        if (e.act != Z1_ACT_NONE)
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                v[j] = act_value(e.act, v[j]);
+        act_values(e.act, v);
         if (e.mul) {
             get(e.mul, row * e.ld_mul + col, n, a);
 #pragma unroll
@@ -295,38 +316,94 @@ constexpr int kGroup = 8;
     tq = (int32_t)(first + id % high);
 }
 
-// One TILE x TILE tile of C, one 64-byte deep panel after another, in a ring of
-// RING panels, so that RING - 1 are on their way while one is multiplied.
-// PAIRED (256 tiles, 8 waves, one workgroup a compute unit): waves w and w + 4
-// share a SIMD, and the second four run half a step behind the first, so that
-// one of the two multiplies while the other reads its fragments and issues
-// copies; two barriers a panel keep them in step.
-template <typename E, bool PD, bool QD, int TILE, int WP, int WQ, int PANELS, int RING, bool PAIRED, typename OUT>
-__global__ __launch_bounds__(64 * WP * WQ) void k_product(Product g)
+// The fragments of part kk of a panel.
+template <typename SP, typename SQ, int TP, int TQ>
+__device__ __forceinline__ void read_part(const lds_char *p, const lds_char *q, const int (&pat)[TP], const int (&qat)[TQ],
+                                          int kk, uint4v (&a)[TP], uint4v (&b)[TQ])
+{
+#pragma unroll
+    for (int j = 0; j < TQ; ++j)
+        b[j] = SQ::frag(q, qat[j], kk);
+#pragma unroll
+    for (int i = 0; i < TP; ++i)
+        a[i] = SP::frag(p, pat[i], kk);
+}
+
+template <typename E, int TP, int TQ>
+__device__ __forceinline__ void multiply(float16v (&acc)[TP][TQ], const uint4v (&a)[TP], const uint4v (&b)[TQ])
+{
+#pragma unroll
+    for (int i = 0; i < TP; ++i)
+#pragma unroll
+        for (int j = 0; j < TQ; ++j)
+            mma(E(), acc[i][j], a[i], b[j]);
+}
+
+// One panel after another, in a ring of RING, so that RING - 1 are on their way while
+// one is multiplied.
+template <typename E, typename SP, typename SQ, int TP, int TQ, int RING>
+__device__ __forceinline__ void ring_loop(lds_char *__restrict__ to, const lds_char *__restrict__ from, SP &sp, SQ &sq,
+                                          const int (&pat)[TP], const int (&qat)[TQ], float16v (&acc)[TP][TQ], int panels,
+                                          int wave)
+{
+    constexpr int kAhead = (RING - 2) * (SP::kLoads + SQ::kLoads);   // copies that may stay out at a wait
+    constexpr int kBytes = SP::kBytes + SQ::kBytes, kParts = SP::kParts;
+#pragma unroll
+    for (int s = 0; s < RING - 1; ++s)
+        if (s < panels) {
+            sp.load(to + s * kBytes, wave);
+            sq.load(to + s * kBytes + SP::kBytes, wave);
+        }
+    int slot = 0;
+    for (int k = 0; k < panels; ++k) {
+        // panel k has arrived, and every wave has read panel k - 1, whose slot the
+        // next copy overwrites
+        if (k + RING - 2 < panels)
+            wait_copies<kAhead>();
+        else
+            wait_copies<0>();
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        if (k + RING - 1 < panels) {
+            const int next = slot == 0 ? RING - 1 : slot - 1;
+            sp.load(to + next * kBytes, wave);
+            sq.load(to + next * kBytes + SP::kBytes, wave);
+        }
+        uint4v a[kParts][TP], b[kParts][TQ];
+        const lds_char *at = from + slot * kBytes;
+#pragma unroll
+        for (int kk = 0; kk < kParts; ++kk)
+            read_part<SP, SQ>(at, at + SP::kBytes, pat, qat, kk, a[kk], b[kk]);
+#pragma unroll
+        for (int kk = 0; kk < kParts; ++kk)
+            multiply<E>(acc, a[kk], b[kk]);
+        slot = slot + 1 == RING ? 0 : slot + 1;
+    }
+}
+
+// One TILE x TILE tile of C (64 or 128), or one piece of its depth.
+template <typename E, bool PD, bool QD, int TILE, int DB, int RING, typename OUT>
+__global__ __launch_bounds__(256) void k_product(Product g)
 {
 #if defined(__HIP_DEVICE_COMPILE__)   // the host's pass does not know the matrix and LDS builtins
-    constexpr int NW = WP * WQ;
-    constexpr int TP = TILE / WP / 32, TQ = TILE / WQ / 32;
-    static_assert(!PAIRED || PANELS == 1, "one panel a phase");
-    typedef Side<E, PD, TILE, NW> SP;
-    typedef Side<E, QD, TILE, NW> SQ;
-    constexpr int kShare = TILE * 64;
-    constexpr int kAhead = (RING - 2) * PANELS * (SP::kLoads + SQ::kLoads);   // copies that may stay out at a wait
-    __shared__ __align__(1024) char lds[RING][PANELS][2][kShare];
+    constexpr int TP = TILE / 64, TQ = TILE / 64;   // 2 x 2 waves
+    typedef Side<E, PD, TILE, 4, DB> SP;
+    typedef Side<E, QD, TILE, 4, DB> SQ;
+    __shared__ __align__(1024) char lds[RING * (SP::kBytes + SQ::kBytes)];
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wp = wave / WQ, wq = wave % WQ;
+    const int wp = wave >> 1, wq = wave & 1;
     int32_t tp, tq, piece;
     tile_of(g, blockIdx.x, gridDim.x, tp, tq, piece);
 
     SP sp;
     SQ sq;
-    const int32_t first = piece * g.piece;
+    const int32_t per = g.piece / DB, first = piece * per;
     sp.start(g.p, tp, first, wave, lane);
     sq.start(g.q, tq, first, wave, lane);
-    const int32_t panels = min(g.piece, (g.p.depth + SP::kPanel - 1) / SP::kPanel - first);
-    const int steps = (panels + PANELS - 1) / PANELS;
+    const int32_t panels = min(per, (g.p.depth + SP::kPanel - 1) / SP::kPanel - first);
 
     int pat[TP], qat[TQ];
 #pragma unroll
@@ -335,11 +412,6 @@ __global__ __launch_bounds__(64 * WP * WQ) void k_product(Product g)
 #pragma unroll
     for (int j = 0; j < TQ; ++j)
         qat[j] = SQ::place((wq * TQ + j) * 32, lane);
-
-    const auto load = [&](int slot, int panel) {
-        sp.load(lds[slot][panel][0], wave);
-        sq.load(lds[slot][panel][1], wave);
-    };
 
     float16v acc[TP][TQ];
 #pragma unroll
@@ -350,81 +422,7 @@ __global__ __launch_bounds__(64 * WP * WQ) void k_product(Product g)
             for (int r = 0; r < 16; ++r)
                 acc[i][j][r] = 0.f;
 
-#pragma unroll
-    for (int s = 0; s < RING - 1; ++s)
-        if (s < steps)
-#pragma unroll
-            for (int p = 0; p < PANELS; ++p)
-                load(s, p);
-    if (PAIRED) {
-        if (steps >= RING - 1)
-            wait_copies<kAhead>();
-        else
-            wait_copies<0>();
-        __builtin_amdgcn_s_barrier();
-        if (wave >= NW / 2)
-            __builtin_amdgcn_s_barrier();
-    }
-    int slot = 0;
-    for (int k = 0; k < steps; ++k) {
-        const int next = slot == 0 ? RING - 1 : slot - 1;   // the slot of step k + RING - 1
-        const bool more = k + RING - 1 < steps;
-        if (!PAIRED) {
-            // panel k has arrived, and every wave has read panel k - 1, whose
-            // slot the next copy overwrites
-            if (k + RING - 2 < steps)
-                wait_copies<kAhead>();
-            else
-                wait_copies<0>();
-            __builtin_amdgcn_s_barrier();
-            asm volatile("" ::: "memory");
-            if (more)
-#pragma unroll
-                for (int p = 0; p < PANELS; ++p)
-                    load(next, p);
-        }
-        uint4v a[2 * PANELS][TP], b[2 * PANELS][TQ];
-        asm volatile("" ::: "memory");
-#pragma unroll
-        for (int kk = 0; kk < 2 * PANELS; ++kk) {
-#pragma unroll
-            for (int j = 0; j < TQ; ++j)
-                b[kk][j] = SQ::frag(lds[slot][kk >> 1][1], qat[j], kk & 1);
-#pragma unroll
-            for (int i = 0; i < TP; ++i)
-                a[kk][i] = SP::frag(lds[slot][kk >> 1][0], pat[i], kk & 1);
-        }
-        if (PAIRED) {
-            // the slot being filled was last read in panel k - 1, by both
-            // halves before the barrier that ended their reads of it
-            if (more)
-                load(next, 0);
-            asm volatile("" ::: "memory");
-            // panel k + 1 has arrived once every wave is past this barrier
-            if (more)
-                wait_copies<kAhead>();
-            else
-                wait_copies<0>();
-            __builtin_amdgcn_s_barrier();
-            __builtin_amdgcn_sched_barrier(0);
-        }
-#pragma unroll
-        for (int kk = 0; kk < 2 * PANELS; ++kk)
-#pragma unroll
-            for (int i = 0; i < TP; ++i)
-#pragma unroll
-                for (int j = 0; j < TQ; ++j)
-                    mma(E(), acc[i][j], a[kk][i], b[kk][j]);
-        if (PAIRED) {
-            __builtin_amdgcn_sched_barrier(0);
-            __builtin_amdgcn_s_barrier();
-            __builtin_amdgcn_sched_barrier(0);
-        }
-        asm volatile("" ::: "memory");
-        slot = slot + 1 == RING ? 0 : slot + 1;
-    }
-    if (PAIRED && wave < NW / 2)
-        __builtin_amdgcn_s_barrier();   // as many as the second four
+    ring_loop<E, SP, SQ, TP, TQ, RING>((lds_char *)&lds[0], hidden((const lds_char *)&lds[0]), sp, sq, pat, qat, acc, panels, wave);
 
     if (g.splits > 1) {
         float *to = g.parts + ((int64_t)piece * g.tiles_p * g.tiles_q + (int64_t)tq * g.tiles_p + tp) * TILE * TILE +
@@ -450,6 +448,176 @@ __global__ __launch_bounds__(64 * WP * WQ) void k_product(Product g)
                 v[r] = float4v{acc[i][j][4 * r], acc[i][j][4 * r + 1], acc[i][j][4 * r + 2], acc[i][j][4 * r + 3]};
             put_block<OUT>(g, key, (int64_t)tq * TILE + (wq * TQ + j) * 32, (int64_t)tp * TILE + (wp * TP + i) * 32, lane, v);
         }
+#endif
+}
+
+// READS LDS reads in front of each of four matrix instructions, then two copies with one
+// behind each.
+template <int READS>
+__device__ __forceinline__ void half_order()
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x100, READS, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    }
+}
+
+// A quarter of a panel of k_product_256: multiplies a0 b0, reads the fragments of part
+// kk of the panel at p and q, and makes four of the wave's copies of side C's next
+// panel, from copy FROM on.  The scheduler is given the order: P's reads between the
+// first four of the 16 matrix instructions, two copies, Q's reads, two copies.  (Reads
+// and copies stay in the order written, as the compiler does not tell a transposing
+// read from what a copy writes.)
+template <typename E, typename SP, typename SQ, int T, int FROM, typename SC>
+__device__ __forceinline__ void quarter(const lds_char *p, const lds_char *q, const int (&pat)[T], const int (&qat)[T], int kk,
+                                        uint4v (&a)[T], uint4v (&b)[T], lds_char *to, SC &side, int wave,
+                                        float16v (&acc)[T][T], const uint4v (&a0)[T], const uint4v (&b0)[T])
+{
+#pragma unroll
+    for (int i = 0; i < T; ++i)
+        a[i] = SP::frag(p, pat[i], kk);
+    side.template load<FROM, FROM + 2>(to, wave);
+#pragma unroll
+    for (int j = 0; j < T; ++j)
+        b[j] = SQ::frag(q, qat[j], kk);
+    side.template load<FROM + 2, FROM + 4>(to, wave);
+    multiply<E>(acc, a0, b0);
+    half_order<SP::kReads>();
+    half_order<SQ::kReads>();
+    __builtin_amdgcn_sched_group_barrier(0x008, 4, 0);
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// The same on 256 x 256 tiles with four waves, one a SIMD, each of which holds 128 x
+// 128 of C in 256 registers: 64 bytes of depth then take 64 KiB of LDS reads where
+// eight waves of 128 x 64 take 96, and with the copies' 32 KiB the LDS is busy for
+// three quarters of the time that the matrix instructions take, not for all of it.
+// A wave has nobody to hide its waits, so it runs ahead of itself: the fragments of
+// one quarter of a panel's depth (128 bytes) are read while the one before is
+// multiplied, and the scheduler is told to spread reads and copies between the matrix
+// instructions.
+//
+// One barrier a panel, in front of its last quarter: behind it every wave has all of
+// panel k in registers, and panel k + 1 has arrived.  P has two slots, Q three (160
+// KiB in all).  P of panel k + 1 is copied through the last quarter of panel k - 1 and
+// the first of k, Q of panel k + 2 through the two quarters behind those, one copy to
+// four matrix instructions: the address unit is busy for half of its time with them,
+// and a wave that has to wait for it issues no matrix instruction either.  Copies past
+// the last panel bring zeros and keep the count of outstanding ones even.
+// 8192^3, us: with 64-byte panels, whose deep rows are half a cache line, and all of a
+// panel's copies behind its barrier 904, spread over the panel 899.
+template <typename E, typename SP, typename SQ, int T>
+__device__ __forceinline__ void wide_loop(lds_char *__restrict__ to, const lds_char *__restrict__ from, SP &sp, SQ &sq,
+                                          const int (&pat)[T], const int (&qat)[T], float16v (&acc)[T][T], int panels, int wave)
+{
+    constexpr int kQ = 2 * SP::kBytes;   // Q's slots lie behind P's two
+    static_assert(SP::kLoads == 8 && SQ::kLoads == 8 && T == 4 && SP::kParts == 4, "the schedule below");
+    uint4v a[2][T], b[2][T];
+    sp.load(to, wave);
+    sq.load(to + kQ, wave);
+    sq.load(to + kQ + SQ::kBytes, wave);
+    sp.template load<0, 4>(to + SP::kBytes, wave);
+    wait_copies<12>();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    read_part<SP, SQ>(from, from + kQ, pat, qat, 0, a[0], b[0]);
+    int ps = 0, qs = 0;   // the panel's slots
+    for (int k = 0; k < panels; ++k) {
+        const lds_char *p = from + ps * SP::kBytes, *q = from + kQ + qs * SQ::kBytes;
+        const int before = qs == 0 ? 2 : qs - 1, next = qs == 2 ? 0 : qs + 1;
+        lds_char *const p_other = to + (ps ^ 1) * SP::kBytes, *const q_free = to + kQ + before * SQ::kBytes;
+        quarter<E, SP, SQ, T, 4>(p, q, pat, qat, 1, a[1], b[1], p_other, sp, wave, acc, a[0], b[0]);
+        quarter<E, SP, SQ, T, 0>(p, q, pat, qat, 2, a[0], b[0], q_free, sq, wave, acc, a[1], b[1]);
+        quarter<E, SP, SQ, T, 4>(p, q, pat, qat, 3, a[1], b[1], q_free, sq, wave, acc, a[0], b[0]);
+        wait_copies<8>();
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+        quarter<E, SP, SQ, T, 0>(from + (ps ^ 1) * SP::kBytes, from + kQ + next * SQ::kBytes, pat, qat, 0, a[0], b[0],
+                                 to + ps * SP::kBytes, sp, wave, acc, a[1], b[1]);
+        ps ^= 1;
+        qs = next;
+    }
+}
+
+template <typename E, bool PD, bool QD, typename OUT>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) void k_product_256(Product g)
+{
+#if defined(__HIP_DEVICE_COMPILE__)
+    constexpr int TILE = 256, T = 4;
+    typedef Side<E, PD, TILE, 4, 128> SP;
+    typedef Side<E, QD, TILE, 4, 128> SQ;
+    __shared__ __align__(1024) char lds[2 * SP::kBytes + 3 * SQ::kBytes];
+
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wp = wave >> 1, wq = wave & 1;
+    int32_t tp, tq, piece;
+    tile_of(g, blockIdx.x, gridDim.x, tp, tq, piece);
+    SP sp;
+    SQ sq;
+    sp.start(g.p, tp, 0, wave, lane);
+    sq.start(g.q, tq, 0, wave, lane);
+    const int32_t panels = (g.p.depth + SP::kPanel - 1) / SP::kPanel;
+
+    int pat[T], qat[T];
+#pragma unroll
+    for (int i = 0; i < T; ++i) {
+        pat[i] = SP::place((wp * T + i) * 32, lane);
+        qat[i] = SQ::place((wq * T + i) * 32, lane);
+    }
+    float16v acc[T][T];
+#pragma unroll
+    for (int i = 0; i < T; ++i)
+#pragma unroll
+        for (int j = 0; j < T; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                acc[i][j][r] = 0.f;
+
+    wide_loop<E, SP, SQ, T>((lds_char *)&lds[0], hidden((const lds_char *)&lds[0]), sp, sq, pat, qat, acc, panels, wave);
+    wait_copies<0>();   // what still comes must not fall into what the LDS holds next
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+
+    // 32 rows of C at a time through the wave's own part of the LDS, so that 16
+    // lanes write 128 elements of a row together.  Rows are 16 bytes longer than
+    // their data, which spreads both accesses over the banks.
+    const DropKey key = OUT::kDrops ? drop_key(g.e.drop) : DropKey{};
+    constexpr int kRowBytes = 128 * 4 + 16;
+    static_assert(4 * 32 * kRowBytes <= (int)sizeof(lds), "a strip for each wave");
+    char *own = &lds[0] + wave * 32 * kRowBytes;
+    const int half = lane >> 5, low = lane & 31;
+    const int64_t p0 = (int64_t)tp * TILE + wp * 128 + (lane & 15) * 8;
+    const int n = (int)min((int64_t)8, g.P - p0);
+#pragma unroll
+    for (int j = 0; j < T; ++j) {
+        asm volatile("" ::: "memory");
+#pragma unroll
+        for (int i = 0; i < T; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                *reinterpret_cast<float4v *>(own + low * kRowBytes + (i * 32 + 8 * r + 4 * half) * 4) =
+                    float4v{acc[i][j][4 * r], acc[i][j][4 * r + 1], acc[i][j][4 * r + 2], acc[i][j][4 * r + 3]};
+        asm volatile("" ::: "memory");   // a wave's LDS accesses take place in order
+        const int64_t q0 = (int64_t)tq * TILE + (wq * T + j) * 32 + (lane >> 4);
+#pragma unroll 1
+        for (int r = 0; r < 8; ++r) {
+            const char *from = own + ((lane >> 4) + 4 * r) * kRowBytes + (lane & 15) * 32;
+            const float4v x = reinterpret_cast<const float4v *>(from)[0], y = reinterpret_cast<const float4v *>(from)[1];
+            float v[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+            if (n > 0 && q0 + 4 * r < g.Q)
+                OUT::put(g.e, key, q0 + 4 * r, (int32_t)p0, n, v);
+        }
+    }
 #endif
 }
 
@@ -482,11 +650,11 @@ hipError_t products(const Product &g, hipStream_t s)
     const uint32_t tiles = (uint32_t)g.tiles_p * (uint32_t)g.tiles_q, n = tiles * (uint32_t)g.splits;
     if (g.tile == 256) {
         if constexpr (sizeof(typename E::store) == 2)
-            k_product<E, PD, QD, 256, 2, 4, 1, 4, true, OUT><<<n, 512, 0, s>>>(g);
+            k_product_256<E, PD, QD, OUT><<<n, 256, 0, s>>>(g);
     } else if (g.tile == 128) {
-        k_product<E, PD, QD, 128, 2, 2, 1, 3, false, OUT><<<n, 256, 0, s>>>(g);
+        k_product<E, PD, QD, 128, 64, 3, OUT><<<n, 256, 0, s>>>(g);
     } else {
-        k_product<E, PD, QD, 64, 2, 2, 2, 3, false, OUT><<<n, 256, 0, s>>>(g);
+        k_product<E, PD, QD, 64, 128, 3, OUT><<<n, 256, 0, s>>>(g);
         if (g.splits > 1)
             k_product_join<OUT><<<tiles, 256, 0, s>>>(g);
     }
