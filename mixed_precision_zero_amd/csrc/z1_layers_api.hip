@@ -6,6 +6,7 @@
 #include "z1_host.h"
 #include "z1_layers.h"
 #include "z1_layers_internal.h"
+#include "z1_linear_tile.h"
 
 using namespace z1::host;
 using z1::ops::Drop;
@@ -89,18 +90,12 @@ Plan plan_product(Form form, int32_t dtype, const Matrix &p, const Matrix &q)
     g.P = (int32_t)(p_deep ? p.rows : p.cols);
     g.Q = (int32_t)(q_deep ? q.rows : q.cols);
     const int64_t bytes = std::max(g.p.depth, g.q.depth) * size;   // of depth
-    const auto tiles = [&](int64_t side) { return ((g.P + side - 1) / side) * ((g.Q + side - 1) / side); };
-    // the largest tile that still gives most compute units one
-    g.tile = dtype != Z1_F32 && tiles(256) >= 160 ? 256 : tiles(128) >= 200 ? 128 : 64;
+    const z1::ops::TileChoice c = z1::ops::pick_product(g.P, g.Q, bytes, dtype == Z1_F32);
+    g.tile = c.tile;
+    g.splits = c.splits;
+    g.piece = c.piece;
     g.tiles_p = (g.P + g.tile - 1) / g.tile;
     g.tiles_q = (g.Q + g.tile - 1) / g.tile;
-    g.splits = 1;
-    if (g.tile == 64) {
-        const int64_t n = tiles(64);
-        g.splits = (int32_t)std::max<int64_t>(1, std::min<int64_t>({512 / std::max<int64_t>(1, n), bytes / 512, 64}));
-    }
-    g.piece = (int32_t)pad_to(std::max<int64_t>(1, (bytes + g.splits - 1) / g.splits), 128);
-    g.splits = (int32_t)std::max<int64_t>(1, (bytes + g.piece - 1) / g.piece);
     if (g.splits > 1) {
         w.at_parts = w.bytes;
         w.bytes += (int64_t)g.splits * g.tiles_p * g.tiles_q * g.tile * g.tile * 4;

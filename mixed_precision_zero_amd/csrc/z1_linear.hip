@@ -382,38 +382,40 @@ __device__ __forceinline__ void ring_loop(lds_char *__restrict__ to, const lds_c
     }
 }
 
-// One TILE x TILE tile of C (64 or 128), or one piece of its depth.
-template <typename E, bool PD, bool QD, int TILE, int DB, int RING, typename OUT>
-__global__ __launch_bounds__(256) void k_product(Product g)
-{
-#if defined(__HIP_DEVICE_COMPILE__)   // the host's pass does not know the matrix and LDS builtins
-    constexpr int TP = TILE / 64, TQ = TILE / 64;   // 2 x 2 waves
-    typedef Side<E, PD, TILE, 4, DB> SP;
-    typedef Side<E, QD, TILE, 4, DB> SQ;
-    __shared__ __align__(1024) char lds[RING * (SP::kBytes + SQ::kBytes)];
-
-    const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wp = wave >> 1, wq = wave & 1;
-    int32_t tp, tq, piece;
-    tile_of(g, blockIdx.x, gridDim.x, tp, tq, piece);
-
+// What a product's kernel sets up: its tile, its operands' sides, and the places of its
+// wave's fragments; and what it does with its sums.
+template <typename SP, typename SQ, int TILE, int TP, int TQ>
+struct Setup {
     SP sp;
     SQ sq;
-    const int32_t per = g.piece / DB, first = piece * per;
-    sp.start(g.p, tp, first, wave, lane);
-    sq.start(g.q, tq, first, wave, lane);
-    const int32_t panels = min(per, (g.p.depth + SP::kPanel - 1) / SP::kPanel - first);
-
+    int32_t tp, tq, piece, panels;
+    int lane, wave, wp, wq;
     int pat[TP], qat[TQ];
-#pragma unroll
-    for (int i = 0; i < TP; ++i)
-        pat[i] = SP::place((wp * TP + i) * 32, lane);
-#pragma unroll
-    for (int j = 0; j < TQ; ++j)
-        qat[j] = SQ::place((wq * TQ + j) * 32, lane);
 
-    float16v acc[TP][TQ];
+    __device__ __forceinline__ void start(const Product &g)
+    {
+        constexpr int DB = SP::kParts * 32;
+        lane = threadIdx.x & 63;
+        wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        wp = wave >> 1;
+        wq = wave & 1;
+        tile_of(g, blockIdx.x, gridDim.x, tp, tq, piece);
+        const int32_t per = g.piece / DB, first = piece * per;
+        sp.start(g.p, tp, first, wave, lane);
+        sq.start(g.q, tq, first, wave, lane);
+        panels = min(per, (g.p.depth + SP::kPanel - 1) / SP::kPanel - first);
+#pragma unroll
+        for (int i = 0; i < TP; ++i)
+            pat[i] = SP::place((wp * TP + i) * 32, lane);
+#pragma unroll
+        for (int j = 0; j < TQ; ++j)
+            qat[j] = SQ::place((wq * TQ + j) * 32, lane);
+    }
+};
+
+template <int TP, int TQ>
+__device__ __forceinline__ void clear(float16v (&acc)[TP][TQ])
+{
 #pragma unroll
     for (int i = 0; i < TP; ++i)
 #pragma unroll
@@ -421,33 +423,191 @@ __global__ __launch_bounds__(256) void k_product(Product g)
 #pragma unroll
             for (int r = 0; r < 16; ++r)
                 acc[i][j][r] = 0.f;
+}
 
-    ring_loop<E, SP, SQ, TP, TQ, RING>((lds_char *)&lds[0], hidden((const lds_char *)&lds[0]), sp, sq, pat, qat, acc, panels, wave);
-
-    if (g.splits > 1) {
-        float *to = g.parts + ((int64_t)piece * g.tiles_p * g.tiles_q + (int64_t)tq * g.tiles_p + tp) * TILE * TILE +
-                    wave * TP * TQ * 1024 + lane * 4;
-#pragma unroll
-        for (int i = 0; i < TP; ++i)
-#pragma unroll
-            for (int j = 0; j < TQ; ++j)
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    *reinterpret_cast<float4v *>(to + (i * TQ + j) * 1024 + r * 256) =
-                        float4v{acc[i][j][4 * r], acc[i][j][4 * r + 1], acc[i][j][4 * r + 2], acc[i][j][4 * r + 3]};
-        return;
-    }
-    const DropKey key = OUT::kDrops ? drop_key(g.e.drop) : DropKey{};
+// The sums of one piece of a split product, for k_product_join: 16 bytes a lane.
+template <int TILE, int TP, int TQ>
+__device__ __forceinline__ void put_parts(const Product &g, int32_t tp, int32_t tq, int32_t piece, int wave, int lane,
+                                          const float16v (&acc)[TP][TQ])
+{
+    float *to = g.parts + ((int64_t)piece * g.tiles_p * g.tiles_q + (int64_t)tq * g.tiles_p + tp) * TILE * TILE +
+                wave * TP * TQ * 1024 + lane * 4;
 #pragma unroll
     for (int i = 0; i < TP; ++i)
 #pragma unroll
-        for (int j = 0; j < TQ; ++j) {
-            float4v v[4];
+        for (int j = 0; j < TQ; ++j)
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-                v[r] = float4v{acc[i][j][4 * r], acc[i][j][4 * r + 1], acc[i][j][4 * r + 2], acc[i][j][4 * r + 3]};
-            put_block<OUT>(g, key, (int64_t)tq * TILE + (wq * TQ + j) * 32, (int64_t)tp * TILE + (wp * TP + i) * 32, lane, v);
+                *reinterpret_cast<float4v *>(to + (i * TQ + j) * 1024 + r * 256) =
+                    float4v{acc[i][j][4 * r], acc[i][j][4 * r + 1], acc[i][j][4 * r + 2], acc[i][j][4 * r + 3]};
+}
+
+// A wave's sums into C, 32 rows of C at a time through its own part of the LDS, so that
+// TP * 4 lanes write TP * 32 elements of a row together.  Rows are 16 bytes longer than
+// their data, which spreads both accesses over the banks.
+template <typename OUT, int TILE, int TP, int TQ>
+__device__ __forceinline__ void put_strips(const Product &g, int32_t tp, int32_t tq, int wp, int wq, int wave, int lane,
+                                           char *lds, const float16v (&acc)[TP][TQ])
+{
+    constexpr int kRowBytes = TP * 128 + 16, kLanes = TP * 4, kRows = 64 / kLanes;
+    const DropKey key = OUT::kDrops ? drop_key(g.e.drop) : DropKey{};
+    char *own = lds + wave * 32 * kRowBytes;
+    const int half = lane >> 5, low = lane & 31, at = lane % kLanes, row = lane / kLanes;
+    const int64_t p0 = (int64_t)tp * TILE + wp * TP * 32 + at * 8;
+    const int n = (int)min((int64_t)8, g.P - p0);
+#pragma unroll
+    for (int j = 0; j < TQ; ++j) {
+        asm volatile("" ::: "memory");
+#pragma unroll
+        for (int i = 0; i < TP; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                *reinterpret_cast<float4v *>(own + low * kRowBytes + (i * 32 + 8 * r + 4 * half) * 4) =
+                    float4v{acc[i][j][4 * r], acc[i][j][4 * r + 1], acc[i][j][4 * r + 2], acc[i][j][4 * r + 3]};
+        asm volatile("" ::: "memory");   // a wave's LDS accesses take place in order
+        const int64_t q0 = (int64_t)tq * TILE + (wq * TQ + j) * 32 + row;
+#pragma unroll 1
+        for (int r = 0; r < 32; r += kRows) {
+            const char *from = own + (row + r) * kRowBytes + at * 32;
+            const float4v x = reinterpret_cast<const float4v *>(from)[0], y = reinterpret_cast<const float4v *>(from)[1];
+            float v[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+            if (n > 0 && q0 + r < g.Q)
+                OUT::put(g.e, key, q0 + r, (int32_t)p0, n, v);
         }
+    }
+}
+
+// One 64 x 64 tile of C, or one piece of its depth.  Several workgroups a compute unit
+// hide each other's waits.
+template <typename E, bool PD, bool QD, typename OUT>
+__global__ __launch_bounds__(256) void k_product_64(Product g)
+{
+#if defined(__HIP_DEVICE_COMPILE__)   // the host's pass does not know the matrix and LDS builtins
+    constexpr int TILE = 64, RING = 3;
+    typedef Side<E, PD, TILE, 4, 128> SP;
+    typedef Side<E, QD, TILE, 4, 128> SQ;
+    __shared__ __align__(1024) char lds[RING * (SP::kBytes + SQ::kBytes)];
+    Setup<SP, SQ, TILE, 1, 1> u;
+    u.start(g);
+    float16v acc[1][1];
+    clear(acc);
+    ring_loop<E, SP, SQ, 1, 1, RING>((lds_char *)&lds[0], hidden((const lds_char *)&lds[0]), u.sp, u.sq, u.pat, u.qat, acc,
+                                     u.panels, u.wave);
+    if (g.splits > 1) {
+        put_parts<TILE>(g, u.tp, u.tq, u.piece, u.wave, u.lane, acc);
+        return;
+    }
+    const DropKey key = OUT::kDrops ? drop_key(g.e.drop) : DropKey{};
+    float4v v[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+        v[r] = float4v{acc[0][0][4 * r], acc[0][0][4 * r + 1], acc[0][0][4 * r + 2], acc[0][0][4 * r + 3]};
+    put_block<OUT>(g, key, (int64_t)u.tq * TILE + u.wq * 32, (int64_t)u.tp * TILE + u.wp * 32, u.lane, v);
+#endif
+}
+
+// A quarter of a panel of k_product_128: multiplies a0 b0, reads the fragments of part
+// kk of the panel at p and q, and makes the F-th quarter of the wave's copies of a panel
+// on its way to `to`, in the order P's reads, P's copy, Q's reads, Q's copy, spread
+// between the matrix instructions.  (Reads and copies stay in the order written, as the
+// compiler does not tell a transposing read from what a copy writes.)
+template <typename E, typename SP, typename SQ, int F>
+__device__ __forceinline__ void quarter_128(const lds_char *at, const int (&pat)[2], const int (&qat)[2], int kk,
+                                            uint4v (&a)[2], uint4v (&b)[2], lds_char *to, SP &sp, SQ &sq, int wave,
+                                            float16v (&acc)[2][2], const uint4v (&a0)[2], const uint4v (&b0)[2])
+{
+    constexpr int kMma = sizeof(typename E::store) == 4 ? 4 : 1;   // instructions of an mma
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        a[i] = SP::frag(at, pat[i], kk);
+    sp.template load<F, F + 1>(to, wave);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+        b[j] = SQ::frag(at + SP::kBytes, qat[j], kk);
+    sq.template load<F, F + 1>(to + SP::kBytes, wave);
+    multiply<E>(acc, a0, b0);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x100, SP::kReads, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, kMma, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x100, SQ::kReads, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, kMma, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// As wide_loop below, on a ring of RING panels of both operands.
+template <typename E, typename SP, typename SQ, int RING>
+__device__ __forceinline__ void ahead_loop(lds_char *__restrict__ to, const lds_char *__restrict__ from, SP &sp, SQ &sq,
+                                           const int (&pat)[2], const int (&qat)[2], float16v (&acc)[2][2], int panels, int wave)
+{
+    constexpr int kBytes = SP::kBytes + SQ::kBytes, kCopies = SP::kLoads + SQ::kLoads;
+    static_assert(SP::kLoads == 4 && SQ::kLoads == 4 && SP::kParts == 4, "the schedule below");
+    uint4v a[2][2], b[2][2];
+#pragma unroll
+    for (int s = 0; s < RING - 1; ++s) {
+        sp.load(to + s * kBytes, wave);
+        sq.load(to + s * kBytes + SP::kBytes, wave);
+    }
+    sp.template load<0, 1>(to + (RING - 1) * kBytes, wave);
+    sq.template load<0, 1>(to + (RING - 1) * kBytes + SP::kBytes, wave);
+    wait_copies<(RING - 2) * kCopies + kCopies / 4>();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    read_part<SP, SQ>(from, from + SP::kBytes, pat, qat, 0, a[0], b[0]);
+    for (int k = 0; k < panels; k += RING)
+#pragma unroll
+        for (int slot = 0; slot < RING; ++slot) {
+            const lds_char *at = from + slot * kBytes;
+            const int next = slot == RING - 1 ? 0 : slot + 1, before = slot == 0 ? RING - 1 : slot - 1;
+            if (k + slot < panels) {
+                quarter_128<E, SP, SQ, 1>(at, pat, qat, 1, a[1], b[1], to + before * kBytes, sp, sq, wave, acc, a[0], b[0]);
+                quarter_128<E, SP, SQ, 2>(at, pat, qat, 2, a[0], b[0], to + before * kBytes, sp, sq, wave, acc, a[1], b[1]);
+                quarter_128<E, SP, SQ, 3>(at, pat, qat, 3, a[1], b[1], to + before * kBytes, sp, sq, wave, acc, a[0], b[0]);
+                wait_copies<(RING - 2) * kCopies>();
+                asm volatile("" ::: "memory");
+                __builtin_amdgcn_s_barrier();
+                asm volatile("" ::: "memory");
+                __builtin_amdgcn_sched_barrier(0);
+                quarter_128<E, SP, SQ, 0>(from + next * kBytes, pat, qat, 0, a[0], b[0], to + slot * kBytes, sp, sq, wave, acc,
+                                          a[1], b[1]);
+            }
+        }
+}
+
+// One 128 x 128 tile of C, or one piece of its depth, on four waves of 64 x 64.  A
+// panel's fragment reads and copies keep the LDS busy half again as long as its matrix
+// instructions take.  One workgroup a compute unit; a ring of three panels (four or five
+// make no difference), its slots known to the compiler (2048^3: 22.0 us with slots kept
+// in registers, 21.5 without; 25.3 where a wave reads all of a panel, then multiplies).
+template <typename E, bool PD, bool QD, typename OUT>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) void k_product_128(Product g)
+{
+#if defined(__HIP_DEVICE_COMPILE__)
+    constexpr int TILE = 128, RING = 3;
+    typedef Side<E, PD, TILE, 4, 128> SP;
+    typedef Side<E, QD, TILE, 4, 128> SQ;
+    __shared__ __align__(1024) char lds[RING * (SP::kBytes + SQ::kBytes)];
+    Setup<SP, SQ, TILE, 2, 2> u;
+    u.start(g);
+    float16v acc[2][2];
+    clear(acc);
+    ahead_loop<E, SP, SQ, RING>((lds_char *)&lds[0], hidden((const lds_char *)&lds[0]), u.sp, u.sq, u.pat, u.qat, acc,
+                                u.panels, u.wave);
+    wait_copies<0>();   // what still comes must not fall into what the LDS holds next
+    if (g.splits > 1) {
+        put_parts<TILE>(g, u.tp, u.tq, u.piece, u.wave, u.lane, acc);
+        return;
+    }
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    put_strips<OUT, TILE>(g, u.tp, u.tq, u.wp, u.wq, u.wave, u.lane, &lds[0], acc);
 #endif
 }
 
@@ -552,84 +712,38 @@ template <typename E, bool PD, bool QD, typename OUT>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) void k_product_256(Product g)
 {
 #if defined(__HIP_DEVICE_COMPILE__)
-    constexpr int TILE = 256, T = 4;
+    constexpr int TILE = 256;
     typedef Side<E, PD, TILE, 4, 128> SP;
     typedef Side<E, QD, TILE, 4, 128> SQ;
     __shared__ __align__(1024) char lds[2 * SP::kBytes + 3 * SQ::kBytes];
-
-    const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wp = wave >> 1, wq = wave & 1;
-    int32_t tp, tq, piece;
-    tile_of(g, blockIdx.x, gridDim.x, tp, tq, piece);
-    SP sp;
-    SQ sq;
-    sp.start(g.p, tp, 0, wave, lane);
-    sq.start(g.q, tq, 0, wave, lane);
-    const int32_t panels = (g.p.depth + SP::kPanel - 1) / SP::kPanel;
-
-    int pat[T], qat[T];
-#pragma unroll
-    for (int i = 0; i < T; ++i) {
-        pat[i] = SP::place((wp * T + i) * 32, lane);
-        qat[i] = SQ::place((wq * T + i) * 32, lane);
-    }
-    float16v acc[T][T];
-#pragma unroll
-    for (int i = 0; i < T; ++i)
-#pragma unroll
-        for (int j = 0; j < T; ++j)
-#pragma unroll
-            for (int r = 0; r < 16; ++r)
-                acc[i][j][r] = 0.f;
-
-    wide_loop<E, SP, SQ, T>((lds_char *)&lds[0], hidden((const lds_char *)&lds[0]), sp, sq, pat, qat, acc, panels, wave);
+    Setup<SP, SQ, TILE, 4, 4> u;
+    u.start(g);
+    float16v acc[4][4];
+    clear(acc);
+    wide_loop<E, SP, SQ, 4>((lds_char *)&lds[0], hidden((const lds_char *)&lds[0]), u.sp, u.sq, u.pat, u.qat, acc, u.panels, u.wave);
     wait_copies<0>();   // what still comes must not fall into what the LDS holds next
+    if (g.splits > 1) {
+        put_parts<TILE>(g, u.tp, u.tq, u.piece, u.wave, u.lane, acc);
+        return;
+    }
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-
-    // 32 rows of C at a time through the wave's own part of the LDS, so that 16
-    // lanes write 128 elements of a row together.  Rows are 16 bytes longer than
-    // their data, which spreads both accesses over the banks.
-    const DropKey key = OUT::kDrops ? drop_key(g.e.drop) : DropKey{};
-    constexpr int kRowBytes = 128 * 4 + 16;
-    static_assert(4 * 32 * kRowBytes <= (int)sizeof(lds), "a strip for each wave");
-    char *own = &lds[0] + wave * 32 * kRowBytes;
-    const int half = lane >> 5, low = lane & 31;
-    const int64_t p0 = (int64_t)tp * TILE + wp * 128 + (lane & 15) * 8;
-    const int n = (int)min((int64_t)8, g.P - p0);
-#pragma unroll
-    for (int j = 0; j < T; ++j) {
-        asm volatile("" ::: "memory");
-#pragma unroll
-        for (int i = 0; i < T; ++i)
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                *reinterpret_cast<float4v *>(own + low * kRowBytes + (i * 32 + 8 * r + 4 * half) * 4) =
-                    float4v{acc[i][j][4 * r], acc[i][j][4 * r + 1], acc[i][j][4 * r + 2], acc[i][j][4 * r + 3]};
-        asm volatile("" ::: "memory");   // a wave's LDS accesses take place in order
-        const int64_t q0 = (int64_t)tq * TILE + (wq * T + j) * 32 + (lane >> 4);
-#pragma unroll 1
-        for (int r = 0; r < 8; ++r) {
-            const char *from = own + ((lane >> 4) + 4 * r) * kRowBytes + (lane & 15) * 32;
-            const float4v x = reinterpret_cast<const float4v *>(from)[0], y = reinterpret_cast<const float4v *>(from)[1];
-            float v[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
-            if (n > 0 && q0 + 4 * r < g.Q)
-                OUT::put(g.e, key, q0 + 4 * r, (int32_t)p0, n, v);
-        }
-    }
+    put_strips<OUT, TILE>(g, u.tp, u.tq, u.wp, u.wq, u.wave, u.lane, &lds[0], acc);
 #endif
 }
 
-// C from the pieces' sums, added in order: a wave per 32 x 32 block of a 64 x 64
-// tile, lanes as in the product.
-template <typename OUT>
+// C from the pieces' sums, added in order: a wave per 32 x 32 block of a tile, lanes as
+// in the product.
+template <int TILE, typename OUT>
 __global__ __launch_bounds__(256) void k_product_join(Product g)
 {
+    constexpr int T = TILE / 64;   // blocks of a wave along either side
     const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t tiles = (int64_t)g.tiles_p * g.tiles_q, tile = blockIdx.x;
-    const float *from = g.parts + tile * 4096 + wave * 1024 + lane * 4;
+    const int64_t tiles = (int64_t)g.tiles_p * g.tiles_q;
+    const int64_t block = blockIdx.x * 4ll + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t tile = block / (4 * T * T);
+    const int of = (int)(block % (4 * T * T)), wave = of / (T * T), i = of % (T * T) / T, j = of % T;
+    const float *from = g.parts + block * 1024 + lane * 4;
     float4v s[4];
 #pragma unroll
     for (int r = 0; r < 4; ++r)
@@ -638,25 +752,30 @@ __global__ __launch_bounds__(256) void k_product_join(Product g)
     for (int z = 1; z < g.splits; ++z)
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-            s[r] += *reinterpret_cast<const float4v *>(from + z * tiles * 4096 + r * 256);
+            s[r] += *reinterpret_cast<const float4v *>(from + z * tiles * TILE * TILE + r * 256);
     const DropKey key = OUT::kDrops ? drop_key(g.e.drop) : DropKey{};
     const int64_t tq = tile / g.tiles_p, tp = tile % g.tiles_p;
-    put_block<OUT>(g, key, tq * 64 + (wave & 1) * 32, tp * 64 + (wave >> 1) * 32, lane, s);
+    put_block<OUT>(g, key, tq * TILE + ((wave & 1) * T + j) * 32, tp * TILE + ((wave >> 1) * T + i) * 32, lane, s);
 }
 
 template <typename E, bool PD, bool QD, typename OUT>
 hipError_t products(const Product &g, hipStream_t s)
 {
     const uint32_t tiles = (uint32_t)g.tiles_p * (uint32_t)g.tiles_q, n = tiles * (uint32_t)g.splits;
+    const bool join = g.splits > 1;
     if (g.tile == 256) {
         if constexpr (sizeof(typename E::store) == 2)
             k_product_256<E, PD, QD, OUT><<<n, 256, 0, s>>>(g);
+        if (join)
+            k_product_join<256, OUT><<<tiles * 16, 256, 0, s>>>(g);
     } else if (g.tile == 128) {
-        k_product<E, PD, QD, 128, 64, 3, OUT><<<n, 256, 0, s>>>(g);
+        k_product_128<E, PD, QD, OUT><<<n, 256, 0, s>>>(g);
+        if (join)
+            k_product_join<128, OUT><<<tiles * 4, 256, 0, s>>>(g);
     } else {
-        k_product<E, PD, QD, 64, 128, 3, OUT><<<n, 256, 0, s>>>(g);
-        if (g.splits > 1)
-            k_product_join<OUT><<<tiles, 256, 0, s>>>(g);
+        k_product_64<E, PD, QD, OUT><<<n, 256, 0, s>>>(g);
+        if (join)
+            k_product_join<64, OUT><<<tiles, 256, 0, s>>>(g);
     }
     return hipGetLastError();
 }
