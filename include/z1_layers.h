@@ -111,9 +111,9 @@ typedef struct z1_linear_args {
 } z1_linear_args;
 
 /* Bytes of device workspace the call needs for these sizes, row distances and
- * alignments of x and weight (0 for many): copies of operands whose rows are
- * not 16-byte aligned throughout, and partial sums where a deep product of few
- * tiles is split.  Only sizes, dtype, x, weight and their distances are read. */
+ * alignments of x and weight (0 for many, and for up to 4 rows): copies of
+ * operands whose rows are not 16-byte aligned throughout, and partial sums where
+ * a deep product of few tiles is split.  Only sizes, dtype, x, weight and their distances are read. */
 z1_status z1_linear_workspace(const z1_linear_args *args, int64_t *bytes);
 
 /* workspace: 16-byte aligned, may be NULL where no byte is needed. */

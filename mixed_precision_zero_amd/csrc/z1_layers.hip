@@ -77,21 +77,24 @@ __global__ __launch_bounds__(256) void k_dropout(z1_dropout_args a, Drop d)
 }
 
 // --------------------------------------------------------------------------
-// The gradient through the epilogue.  A workgroup takes 256 columns of a piece
-// of the rows (64, more of very many): 32 lanes of eight columns, eight of rows;
-// the column sums of its piece go to a row of `parts`, which k_join adds up.
+// The gradient through the epilogue.  A workgroup takes a piece of the rows of 8 * LX
+// columns: LX lanes of eight columns, 256 / LX of rows; the column sums of its piece go
+// to a row of `parts`, which k_join adds up.  The pieces are as small as 1024 workgroups
+// make them (2048 x 1536 with SILU and a product, bf16: 29 us in pieces of 64 rows, 192
+// workgroups; X in pieces of 16).
 // --------------------------------------------------------------------------
-template <typename T>
+template <typename T, int LX>
 __global__ __launch_bounds__(256) void k_linear_dz(z1_linear_dz_args a, Drop d, float *parts, int64_t piece)
 {
-    __shared__ float lds[8][256];
-    const int cx = threadIdx.x & 31, rx = threadIdx.x >> 5;
-    const int64_t c = blockIdx.x * 256ll + cx * 8, n = a.out - c;
+    constexpr int RX = 256 / LX;
+    __shared__ float lds[RX][LX * 8];
+    const int cx = threadIdx.x % LX, rx = threadIdx.x / LX;
+    const int64_t c = blockIdx.x * (LX * 8ll) + cx * 8, n = a.out - c;
     const int64_t r0 = blockIdx.y * piece, end = min(a.rows, r0 + piece);
     const DropKey key = drop_key(d);
     float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (n > 0) {
-        for (int64_t r = r0 + rx; r < end; r += 8) {
+        for (int64_t r = r0 + rx; r < end; r += RX) {
             float g[8], z[8], m[8];
             get8<T>(a.dy, r * a.ld_dy + c, n, g);
             if (a.pre)
@@ -133,14 +136,28 @@ __global__ __launch_bounds__(256) void k_linear_dz(z1_linear_dz_args a, Drop d, 
     for (int j = 0; j < 8; ++j)
         lds[rx][cx * 8 + j] = sum[j];
     __syncthreads();
-    const int64_t col = blockIdx.x * 256ll + threadIdx.x;
-    if (col < a.out) {
+    const int64_t col = blockIdx.x * (LX * 8ll) + threadIdx.x;
+    if (threadIdx.x < LX * 8 && col < a.out) {
         float s = lds[0][threadIdx.x];
 #pragma unroll
-        for (int q = 1; q < 8; ++q)
+        for (int q = 1; q < RX; ++q)
             s += lds[q][threadIdx.x];
         parts[blockIdx.y * a.out + col] = s;
     }
+}
+
+template <typename T>
+void dz_run(const z1_linear_dz_args &a, const Drop &d, float *parts, hipStream_t s)
+{
+    const int64_t piece = dz_piece(a.rows, a.out);
+    const int lanes = dz_lanes(a.out);
+    const dim3 grid((uint32_t)((a.out + lanes * 8 - 1) / (lanes * 8)), (uint32_t)((a.rows + piece - 1) / piece));
+    if (lanes == 8)
+        k_linear_dz<T, 8><<<grid, 256, 0, s>>>(a, d, parts, piece);
+    else if (lanes == 16)
+        k_linear_dz<T, 16><<<grid, 256, 0, s>>>(a, d, parts, piece);
+    else
+        k_linear_dz<T, 32><<<grid, 256, 0, s>>>(a, d, parts, piece);
 }
 
 // out[c] (+)= the sum of rows of parts: 64 columns x 16 lanes of rows a
@@ -586,13 +603,12 @@ hipError_t launch_dropout(const z1_dropout_args &a, const Drop &d, hipStream_t s
 
 hipError_t launch_linear_dz(const z1_linear_dz_args &a, const Drop &d, float *parts, hipStream_t s)
 {
-    const int64_t piece = dz_piece(a.rows), pieces = (a.rows + piece - 1) / piece;
+    const int64_t piece = dz_piece(a.rows, a.out), pieces = (a.rows + piece - 1) / piece;
     if (pieces > 0) {
-        const dim3 grid((uint32_t)((a.out + 255) / 256), (uint32_t)pieces);
         switch (a.dtype) {
-        case Z1_F32: k_linear_dz<F32><<<grid, 256, 0, s>>>(a, d, parts, piece); break;
-        case Z1_BF16: k_linear_dz<BF16><<<grid, 256, 0, s>>>(a, d, parts, piece); break;
-        default: k_linear_dz<F16><<<grid, 256, 0, s>>>(a, d, parts, piece); break;
+        case Z1_F32: dz_run<F32>(a, d, parts, s); break;
+        case Z1_BF16: dz_run<BF16>(a, d, parts, s); break;
+        default: dz_run<F16>(a, d, parts, s); break;
         }
     }
     if (a.dbias && (pieces > 0 || !a.accumulate))

@@ -73,6 +73,13 @@ Plan plan_product(Form form, int32_t dtype, const Matrix &p, const Matrix &q)
     Product &g = w.g;
     const bool p_deep = form == z1::ops::kForward, q_deep = form != z1::ops::kWeight;
     const int64_t size = (int64_t)type_size(dtype);
+    if (form == z1::ops::kForward && q.rows <= z1::ops::kRowsMost) {
+        g.p = Operand{p.p, (p.rows == 1 ? p.cols : p.ld) * size, (int32_t)p.rows, (int32_t)p.cols};
+        g.q = Operand{q.p, (q.rows == 1 ? q.cols : q.ld) * size, (int32_t)q.rows, (int32_t)q.cols};
+        g.P = (int32_t)p.rows;
+        g.Q = (int32_t)q.rows;
+        return w;
+    }
     const auto operand = [&](const Matrix &m, bool deep, bool &pack, int64_t &at) {
         pack = !in_place(m, dtype);
         int64_t cols = m.cols, ld = m.ld;
@@ -117,6 +124,8 @@ z1_status run_product(Form form, int32_t dtype, int32_t out_dtype, Plan &w, cons
         e = pack(p, w.at_p, g.p);
     if (e == hipSuccess && w.pack_q)
         e = pack(q, w.at_q, g.q);
+    if (g.tile == 0)
+        return status_of(z1::ops::launch_rows(dtype, g, s));
     g.parts = reinterpret_cast<float *>(base + w.at_parts);
     if (e == hipSuccess)
         e = z1::ops::launch_product(form, dtype, out_dtype, g, s);
@@ -275,7 +284,7 @@ z1_status z1_linear_dz_workspace(int64_t rows, int64_t out, int64_t *bytes)
 {
     if (!bytes || rows < 0 || rows > kMostRows || out < 1 || out > kMostSide)
         return Z1_EINVAL;
-    const int64_t piece = z1::ops::dz_piece(rows);
+    const int64_t piece = z1::ops::dz_piece(rows, out);
     *bytes = (rows + piece - 1) / piece * out * 4;
     return Z1_OK;
 }

@@ -87,33 +87,47 @@ struct Words<4> {
 template <typename T>
 struct Eight {
     typedef typename Words<(int)sizeof(typename T::store)>::four word4;
-    static __device__ __forceinline__ void load(const void *p, float (&v)[8])
+    static constexpr int kWords = (int)sizeof(typename T::store) / 2;   // of 16 bytes
+    typedef uint4v Raw[kWords];
+    static __device__ __forceinline__ void fetch(const void *p, Raw &raw)
+    {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i)
+            raw[i] = static_cast<const word4 *>(p)[i];
+    }
+    static __device__ __forceinline__ void up(const Raw &raw, float (&v)[8])
     {
         union {
-            uint4v raw[sizeof(typename T::store) / 2];
+            Raw raw;
             typename T::store e[8];
         } u;
 #pragma unroll
-        for (int i = 0; i < (int)sizeof(typename T::store) / 2; ++i)
-            u.raw[i] = static_cast<const word4 *>(p)[i];
+        for (int i = 0; i < kWords; ++i)
+            u.raw[i] = raw[i];
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             v[j] = T::up(u.e[j]);
     }
+    static __device__ __forceinline__ void load(const void *p, float (&v)[8])
+    {
+        Raw raw;
+        fetch(p, raw);
+        up(raw, v);
+    }
     static __device__ __forceinline__ void store(void *p, const float (&v)[8])
     {
         union {
-            uint4v raw[sizeof(typename T::store) / 2];
+            Raw raw;
             typename T::store e[8];
         } u;
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             u.e[j] = T::down(v[j]);
 #pragma unroll
-        for (int i = 0; i < (int)sizeof(typename T::store) / 2; ++i)
+        for (int i = 0; i < kWords; ++i)
             static_cast<word4 *>(p)[i] = u.raw[i];
     }
-    // the first n < 8 of them; the others load as zeros
+    // the first n of them, where there are so many; the others load as zeros
     static __device__ __forceinline__ void load_some(const void *p, float (&v)[8], int n)
     {
 #pragma unroll
@@ -231,12 +245,16 @@ struct Product {
     int32_t splits;        // 1: not split
     int32_t piece;         // bytes of depth a piece takes, whole panels
     int32_t tiles_p, tiles_q;
-    int32_t tile;          // side: 64, 128 or 256
+    int32_t tile;          // side: 64, 128 or 256; 0: few rows
 };
 
 enum Form { kForward, kInput, kWeight };   // x W', dz W, dz' x: which operands are deep
 
 hipError_t launch_product(Form form, int32_t dtype, int32_t out_dtype, const Product &g, hipStream_t s);
+
+// x W' of at most kRowsMost rows (tile 0): no copies, no partial sums.
+constexpr int64_t kRowsMost = 4;
+hipError_t launch_rows(int32_t dtype, const Product &g, hipStream_t s);
 
 // Copies rows of `cols` elements to rows of `cols_to`, zeros behind them.
 hipError_t launch_pack(int32_t dtype, const void *from, int64_t ld, void *to, int64_t cols_to, int64_t rows,
@@ -248,8 +266,14 @@ hipError_t launch_pack(int32_t dtype, const void *from, int64_t ld, void *to, in
 
 hipError_t launch_dropout(const z1_dropout_args &a, const Drop &d, hipStream_t s);
 
-// Rows of a piece of z1_linear_dz: each piece leaves one row of column sums.
-inline int64_t dz_piece(int64_t rows) { return std::max<int64_t>(64, pad_to((rows + 1023) / 1024, 8)); }
+// z1_linear_dz: lanes of eight columns a workgroup has, and the rows of its piece, whole
+// groups of 256 / lanes; each piece leaves one row of column sums.
+inline int64_t dz_lanes(int64_t out) { return out <= 64 ? 8 : out <= 128 ? 16 : 32; }
+inline int64_t dz_piece(int64_t rows, int64_t out)
+{
+    const int64_t lanes = dz_lanes(out), across = (out + lanes * 8 - 1) / (lanes * 8);
+    return pad_to(std::max<int64_t>(1, rows * across / 1024), 256 / lanes);
+}
 hipError_t launch_linear_dz(const z1_linear_dz_args &a, const Drop &d, float *parts, hipStream_t s);
 
 // Workgroups of z1_qk_norm_rope_grad, each of which leaves a row of sums for

@@ -190,73 +190,92 @@ __device__ __forceinline__ void wait_copies()
 }
 
 // --------------------------------------------------------------------------
-// Epilogues: eight elements (row, col ..) of C, of which n are inside it.
+// Epilogues: eight elements (row, col ..) of C, of which n are inside it.  What they
+// read of the row (In) is fetched apart, so that it can be on its way early; the bias
+// goes by the column alone.
 // --------------------------------------------------------------------------
+
+template <typename E>
+__device__ __forceinline__ void get_row(const void *p, int64_t at, typename Eight<E>::Raw &raw)
+{
+    Eight<E>::fetch(static_cast<const typename E::store *>(p) + at, raw);
+}
+// The eight values of a fetched row, or those of the row's end.
+template <typename E>
+__device__ __forceinline__ void row_values(const typename Eight<E>::Raw &raw, const void *p, int64_t at, int n, float (&v)[8])
+{
+    if (n >= 8)
+        Eight<E>::up(raw, v);
+    else
+        Eight<E>::load_some(static_cast<const typename E::store *>(p) + at, v, n);
+}
+template <typename E>
+__device__ __forceinline__ void put_row(void *p, int64_t at, int n, const float (&v)[8])
+{
+    typename E::store *to = static_cast<typename E::store *>(p) + at;
+    if (n >= 8)
+        Eight<E>::store(to, v);
+    else
+        Eight<E>::store_some(to, v, n);
+}
 
 template <typename O>
 struct PlainOut {
     static constexpr bool kDrops = false;
-    static __device__ __forceinline__ void put(const Epilogue &e, const DropKey &, int64_t row, int32_t col, int n,
-                                               float (&v)[8])
+    struct In {
+        typename Eight<O>::Raw add;
+    };
+    static __device__ __forceinline__ void bias(const Epilogue &, int32_t, int, float (&)[8]) {}
+    static __device__ __forceinline__ void fetch(const Epilogue &e, int64_t row, int32_t col, In &in)
     {
-        typedef typename O::store store;
-        store *out = static_cast<store *>(e.out) + row * e.ld_out + col;
-        const store *add = static_cast<const store *>(e.add) + row * e.ld_add + col;
-        float a[8];
-        if (n >= 8) {
-            if (e.add) {
-                Eight<O>::load(add, a);
+        if (e.add)
+            get_row<O>(e.add, row * e.ld_add + col, in.add);
+    }
+    static __device__ __forceinline__ void put(const Epilogue &e, const DropKey &, int64_t row, int32_t col, int n, const In &in,
+                                               const float (&)[8], float (&v)[8])
+    {
+        if (e.add) {
+            float a[8];
+            row_values<O>(in.add, e.add, row * e.ld_add + col, n, a);
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    v[j] += a[j];
-            }
-            Eight<O>::store(out, v);
-        } else {
-            if (e.add) {
-                Eight<O>::load_some(add, a, n);
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    v[j] += a[j];
-            }
-            Eight<O>::store_some(out, v, n);
+            for (int j = 0; j < 8; ++j)
+                v[j] += a[j];
         }
+        put_row<O>(e.out, row * e.ld_out + col, n, v);
     }
 };
 
 template <typename E>
 struct FullOut {
     static constexpr bool kDrops = true;
-    static __device__ __forceinline__ void get(const void *p, int64_t at, int n, float (&v)[8])
+    struct In {
+        typename Eight<E>::Raw mul, add;
+    };
+    static __device__ __forceinline__ void bias(const Epilogue &e, int32_t col, int n, float (&b)[8])
     {
-        const typename E::store *from = static_cast<const typename E::store *>(p) + at;
-        if (n >= 8)
-            Eight<E>::load(from, v);
-        else
-            Eight<E>::load_some(from, v, n);
+        if (e.bias && n > 0)
+            Eight<E>::load_some(static_cast<const typename E::store *>(e.bias) + col, b, n);
     }
-    static __device__ __forceinline__ void set(void *p, int64_t at, int n, const float (&v)[8])
+    static __device__ __forceinline__ void fetch(const Epilogue &e, int64_t row, int32_t col, In &in)
     {
-        typename E::store *to = static_cast<typename E::store *>(p) + at;
-        if (n >= 8)
-            Eight<E>::store(to, v);
-        else
-            Eight<E>::store_some(to, v, n);
+        if (e.mul)
+            get_row<E>(e.mul, row * e.ld_mul + col, in.mul);
+        if (e.add)
+            get_row<E>(e.add, row * e.ld_add + col, in.add);
     }
-    static __device__ __forceinline__ void put(const Epilogue &e, const DropKey &key, int64_t row, int32_t col, int n,
-                                               float (&v)[8])
+    static __device__ __forceinline__ void put(const Epilogue &e, const DropKey &key, int64_t row, int32_t col, int n, const In &in,
+                                               const float (&b)[8], float (&v)[8])
     {
         float a[8];
-        if (e.bias) {
-            get(e.bias, col, n, a);
+        if (e.bias)
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                v[j] += a[j];
-        }
+                v[j] += b[j];
         if (e.pre)
-            set(e.pre, row * e.ld_pre + col, n, v);
+            put_row<E>(e.pre, row * e.ld_pre + col, n, v);
         act_values(e.act, v);
         if (e.mul) {
-            get(e.mul, row * e.ld_mul + col, n, a);
+            row_values<E>(in.mul, e.mul, row * e.ld_mul + col, n, a);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 v[j] *= a[j];
@@ -264,14 +283,26 @@ struct FullOut {
         if (key.on)
             drop8(key, (uint32_t)col >> 3, (uint32_t)row, v);
         if (e.add) {
-            get(e.add, row * e.ld_add + col, n, a);
+            row_values<E>(in.add, e.add, row * e.ld_add + col, n, a);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 v[j] += a[j];
         }
-        set(e.out, row * e.ld_out + col, n, v);
+        put_row<E>(e.out, row * e.ld_out + col, n, v);
     }
 };
+
+// Eight elements at once, from what is fetched here.
+template <typename OUT>
+__device__ __forceinline__ void put_now(const Epilogue &e, const DropKey &key, int64_t row, int32_t col, int n, float (&v)[8])
+{
+    typename OUT::In in;
+    float b[8];
+    OUT::bias(e, col, n, b);
+    if (n >= 8)
+        OUT::fetch(e, row, col, in);
+    OUT::put(e, key, row, col, n, in, b, v);
+}
 
 // The 32 x 32 block at (q0, p0) of C as the matrix instruction leaves it: column
 // `low`, rows 8 g + 4 half + r.  Swapping the halves' registers of two g gives
@@ -294,7 +325,7 @@ __device__ __forceinline__ void put_block(const Product &g, const DropKey &key, 
         }
         const int64_t p = p0 + 16 * s + 8 * half;
         if (q < g.Q && p < g.P)
-            OUT::put(g.e, key, q, (int32_t)p, (int)(g.P - p), v);
+            put_now<OUT>(g.e, key, q, (int32_t)p, (int)(g.P - p), v);
     }
 }
 
@@ -444,17 +475,28 @@ __device__ __forceinline__ void put_parts(const Product &g, int32_t tp, int32_t 
 
 // A wave's sums into C, 32 rows of C at a time through its own part of the LDS, so that
 // TP * 4 lanes write TP * 32 elements of a row together.  Rows are 16 bytes longer than
-// their data, which spreads both accesses over the banks.
+// their data, which spreads both accesses over the banks.  What the epilogue reads is
+// fetched kAhead rows early: nothing else hides the wait for it.
 template <typename OUT, int TILE, int TP, int TQ>
 __device__ __forceinline__ void put_strips(const Product &g, int32_t tp, int32_t tq, int wp, int wq, int wave, int lane,
                                            char *lds, const float16v (&acc)[TP][TQ])
 {
-    constexpr int kRowBytes = TP * 128 + 16, kLanes = TP * 4, kRows = 64 / kLanes;
+    constexpr int kRowBytes = TP * 128 + 16, kLanes = TP * 4, kRows = 64 / kLanes, kAhead = 4;
     const DropKey key = OUT::kDrops ? drop_key(g.e.drop) : DropKey{};
     char *own = lds + wave * 32 * kRowBytes;
     const int half = lane >> 5, low = lane & 31, at = lane % kLanes, row = lane / kLanes;
-    const int64_t p0 = (int64_t)tp * TILE + wp * TP * 32 + at * 8;
+    const int64_t p0 = (int64_t)tp * TILE + wp * TP * 32 + at * 8, q0 = (int64_t)tq * TILE + wq * TQ * 32 + row;
     const int n = (int)min((int64_t)8, g.P - p0);
+    float b[8];
+    OUT::bias(g.e, (int32_t)p0, n, b);
+    typename OUT::In in[kAhead];
+    const auto fetch = [&](int r, typename OUT::In &to) {
+        if (n >= 8 && q0 + r < g.Q)
+            OUT::fetch(g.e, q0 + r, (int32_t)p0, to);
+    };
+#pragma unroll
+    for (int f = 0; f < kAhead; ++f)
+        fetch(f * kRows, in[f]);
 #pragma unroll
     for (int j = 0; j < TQ; ++j) {
         asm volatile("" ::: "memory");
@@ -465,14 +507,19 @@ __device__ __forceinline__ void put_strips(const Product &g, int32_t tp, int32_t
                 *reinterpret_cast<float4v *>(own + low * kRowBytes + (i * 32 + 8 * r + 4 * half) * 4) =
                     float4v{acc[i][j][4 * r], acc[i][j][4 * r + 1], acc[i][j][4 * r + 2], acc[i][j][4 * r + 3]};
         asm volatile("" ::: "memory");   // a wave's LDS accesses take place in order
-        const int64_t q0 = (int64_t)tq * TILE + (wq * TQ + j) * 32 + row;
 #pragma unroll 1
         for (int r = 0; r < 32; r += kRows) {
             const char *from = own + (row + r) * kRowBytes + at * 32;
             const float4v x = reinterpret_cast<const float4v *>(from)[0], y = reinterpret_cast<const float4v *>(from)[1];
             float v[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
-            if (n > 0 && q0 + r < g.Q)
-                OUT::put(g.e, key, q0 + r, (int32_t)p0, n, v);
+            const typename OUT::In now = in[0];
+#pragma unroll
+            for (int f = 0; f + 1 < kAhead; ++f)
+                in[f] = in[f + 1];
+            if (j * 32 + r + kAhead * kRows < TQ * 32)
+                fetch(j * 32 + r + kAhead * kRows, in[kAhead - 1]);
+            if (n > 0 && q0 + j * 32 + r < g.Q)
+                OUT::put(g.e, key, q0 + j * 32 + r, (int32_t)p0, n, now, b, v);
         }
     }
 }
@@ -792,6 +839,92 @@ hipError_t product_of(Form form, int32_t out_dtype, const Product &g, hipStream_
     return products<E, false, false, PlainOut<E>>(g, s);
 }
 
+// z1_linear of up to R rows: the weight is read once and everything else is small, so a
+// wave streams two rows of it past x, each lane its groups of eight elements, and the
+// lanes' sums are added up; eight outputs a workgroup go through the epilogue together.
+// Operands at any alignment.  1 x 2048 -> 2048 bf16: 3.x us (split products of 64 tiles
+// and their join 10).
+template <typename E, int R, typename OUT>
+__global__ __launch_bounds__(256) void k_linear_rows(Product g)
+{
+    typedef typename E::store store;
+    __shared__ float sums[R][8];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int32_t col = blockIdx.x * 8, K = g.p.depth;
+    const store *w[2], *x[R];
+#pragma unroll
+    for (int o = 0; o < 2; ++o)
+        w[o] = reinterpret_cast<const store *>(static_cast<const char *>(g.p.base) + min(col + wave * 2 + o, g.P - 1) * g.p.ld);
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+        x[r] = reinterpret_cast<const store *>(static_cast<const char *>(g.q.base) + min(r, g.Q - 1) * g.q.ld);
+    float acc[2][R] = {};
+    const auto add = [&](const float (&a)[2][8], const float (&b)[R][8]) {
+#pragma unroll
+        for (int o = 0; o < 2; ++o)
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    acc[o][r] = fmaf(a[o][j], b[r][j], acc[o][r]);
+    };
+    int32_t k = lane * 8;
+#pragma unroll 4
+    for (; k + 8 <= K; k += 512) {
+        float a[2][8], b[R][8];
+#pragma unroll
+        for (int o = 0; o < 2; ++o)
+            Eight<E>::load(w[o] + k, a[o]);
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            Eight<E>::load(x[r] + k, b[r]);
+        add(a, b);
+    }
+    if (k < K) {
+        float a[2][8], b[R][8];
+#pragma unroll
+        for (int o = 0; o < 2; ++o)
+            Eight<E>::load_some(w[o] + k, a[o], K - k);
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            Eight<E>::load_some(x[r] + k, b[r], K - k);
+        add(a, b);
+    }
+#pragma unroll
+    for (int o = 0; o < 2; ++o)
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+#pragma unroll
+            for (int d = 32; d > 0; d >>= 1)
+                acc[o][r] += __shfl_xor(acc[o][r], d);
+            if (lane == 0)
+                sums[r][wave * 2 + o] = acc[o][r];
+        }
+    __syncthreads();
+    const int r = threadIdx.x;
+    if (r < g.Q) {
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            v[j] = sums[r][j];
+        put_now<OUT>(g.e, drop_key(g.e.drop), r, col, g.P - col, v);
+    }
+}
+
+template <typename E>
+hipError_t rows_of(const Product &g, hipStream_t s)
+{
+    const uint32_t n = (uint32_t)(g.P + 7) / 8;
+    if (g.Q <= 1)
+        k_linear_rows<E, 1, FullOut<E>><<<n, 256, 0, s>>>(g);
+    else if (g.Q <= 2)
+        k_linear_rows<E, 2, FullOut<E>><<<n, 256, 0, s>>>(g);
+    else
+        k_linear_rows<E, kRowsMost, FullOut<E>><<<n, 256, 0, s>>>(g);
+    return hipGetLastError();
+}
+
 // Eight elements of a row each; rows start anywhere and end in zeros.
 template <typename T>
 __global__ __launch_bounds__(256) void k_pack(const void *from, int64_t ld, void *to, int64_t cols_to, int64_t rows, int64_t cols)
@@ -819,6 +952,15 @@ hipError_t launch_product(Form form, int32_t dtype, int32_t out_dtype, const Pro
     case Z1_F32: return product_of<F32>(form, out_dtype, g, s);
     case Z1_BF16: return product_of<BF16>(form, out_dtype, g, s);
     default: return product_of<F16>(form, out_dtype, g, s);
+    }
+}
+
+hipError_t launch_rows(int32_t dtype, const Product &g, hipStream_t s)
+{
+    switch (dtype) {
+    case Z1_F32: return rows_of<F32>(g, s);
+    case Z1_BF16: return rows_of<BF16>(g, s);
+    default: return rows_of<F16>(g, s);
     }
 }
 

@@ -12,8 +12,8 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from .binding import LIB_PATH, _check, _dptr, lib
-from .ops import DTYPES, _checked, _dtype_of, _itype_of, _rows_of, _stream
+from .binding import LIB_PATH, _check, lib
+from .ops import DTYPES, _checked, _dtype_of, _itype_of, _on_gpu, _rows_of, _stream
 
 EXPORTS = ("z1_layers_abi_version", "z1_dropout", "z1_linear_workspace", "z1_linear", "z1_linear_dz_workspace",
            "z1_linear_dz", "z1_linear_grad_workspace", "z1_linear_grad", "z1_qk_norm_rope",
@@ -104,30 +104,71 @@ class Dropout(NamedTuple):
     offset: int = 0
 
 
-def _drop_of(d: Optional[Dropout], items: list) -> Drop:
-    if d is None:
-        return Drop(None, 0, 0.0)
-    if not isinstance(d.rng, torch.Tensor) or d.rng.dtype not in (torch.int64, torch.uint64):
-        raise TypeError("dropout.rng: expected a torch tensor of int64 or uint64")
-    items.append((d.rng, "dropout.rng", d.rng.dtype, 2))
-    return Drop(d.rng.data_ptr(), int(d.offset) & 0xffffffffffffffff, float(d.p))
+class _Call:
+    """The checks of one call.  What is right in every respect (type, shape, dense
+    rows, the first tensor's device) takes few calls into torch, as a small layer
+    takes less time than its checks; anything else goes through the full ones,
+    which raise what is wrong with it.  Devices come last, as one reads types and
+    shapes first."""
+
+    __slots__ = ("here", "odd")
+
+    def __init__(self, lead):
+        self.here = lead.get_device()
+        self.odd = [] if self.here >= 0 else [(lead, "the first tensor")]
+
+    def matrix(self, t, name: str, dtype, shape):
+        """(address, distance of rows) of a matrix, or (None, 0)."""
+        if t is None:
+            return None, 0
+        if getattr(t, "dtype", None) is dtype and t.shape == shape and t.is_contiguous():
+            ld = shape[1]
+        else:
+            ld = _rows_of(t, name, dtype, shape)
+        if t.get_device() != self.here:
+            self.odd.append((t, name))
+        return t.data_ptr(), ld
+
+    def vector(self, t, name: str, dtype, need: int):
+        """Address of a contiguous tensor of at least `need` elements, or None."""
+        if t is None:
+            return None
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name}: expected a torch tensor, got {type(t).__name__}")
+        if t.dtype is not dtype or not t.is_contiguous() or t.numel() < need or t.get_device() != self.here:
+            _checked([(t, name, dtype, need)])
+            self.odd.append((t, name))
+        return t.data_ptr()
+
+    def workspace(self, t):
+        """(address, bytes) of a workspace, or (None, 0)."""
+        if t is None:
+            return None, 0
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"workspace: expected a torch tensor, got {type(t).__name__}")
+        n = t.numel() * t.element_size()
+        if n == 0:
+            return None, 0
+        if not t.is_contiguous() or t.get_device() != self.here:
+            _checked([(t, "workspace", None, 0)])
+            self.odd.append((t, "workspace"))
+        return t.data_ptr(), n
+
+    def dropout(self, d: Optional[Dropout]) -> Drop:
+        if d is None:
+            return _NO_DROP
+        if not isinstance(d.rng, torch.Tensor) or d.rng.dtype not in (torch.int64, torch.uint64):
+            raise TypeError("dropout.rng: expected a torch tensor of int64 or uint64")
+        return Drop(self.vector(d.rng, "dropout.rng", d.rng.dtype, 2), d.offset & 0xffffffffffffffff, d.p)
+
+    def done(self):
+        """Every tensor on the current GPU."""
+        if self.odd or torch._C._cuda_getDevice() != self.here:
+            _on_gpu(self.odd)
+            raise ValueError(f"the tensors are on cuda:{self.here}, which is not the current GPU")
 
 
-def _bytes_of(workspace) -> int:
-    if workspace is None:
-        return 0
-    if not isinstance(workspace, torch.Tensor):
-        raise TypeError(f"workspace: expected a torch tensor, got {type(workspace).__name__}")
-    return workspace.numel() * workspace.element_size()
-
-
-def _matrix(t, name: str, rows: list, dtype=None, shape=None):
-    """(address, distance of rows) of a matrix or (None, 0)."""
-    if t is None:
-        return None, 0
-    ld = _rows_of(t, name, dtype, shape)
-    rows.append((t, name))
-    return t.data_ptr(), ld
+_NO_DROP = Drop(None, 0, 0.0)
 
 
 def _act_of(act: str) -> int:
@@ -144,13 +185,13 @@ def z1_dropout(x, y, dropout: Dropout, *, residual=None, stream=None) -> None:
     """y = residual + drop(x) (residual None: drop(x)) of 2-D tensors of one
     type; y may be x or residual.  The gradient is the same call on dy."""
     dt = _dtype_of(x, "x")
-    items, rows = [], []
-    px, ld_x = _matrix(x, "x", rows)
-    py, ld_y = _matrix(y, "y", rows, x.dtype, x.shape)
-    pr, ld_r = _matrix(residual, "residual", rows, x.dtype, x.shape)
-    drop = _drop_of(dropout, items)
-    _checked(items, rows)
-    a = DropoutArgs(x.shape[0], x.shape[1], px, pr, py, ld_x, ld_r, ld_y, drop, dt, 0)
+    ld_x = _rows_of(x, "x")
+    call, shape, kind = _Call(x), x.shape, x.dtype
+    py, ld_y = call.matrix(y, "y", kind, shape)
+    pr, ld_r = call.matrix(residual, "residual", kind, shape)
+    drop = call.dropout(dropout)
+    call.done()
+    a = DropoutArgs(shape[0], shape[1], x.data_ptr(), pr, py, ld_x, ld_r, ld_y, drop, dt, 0)
     _check(lib.z1_dropout(ctypes.byref(a), _stream(stream)), "z1_dropout")
 
 
@@ -158,20 +199,26 @@ def z1_dropout(x, y, dropout: Dropout, *, residual=None, stream=None) -> None:
 # linear
 # --------------------------------------------------------------------------
 
-def _linear_args(x, weight, rows: list) -> LinearArgs:
+def _operands(x, weight):
+    """(the call, dtype, rows, in, out, distances of x's and weight's rows)"""
     dt = _dtype_of(x, "x")
-    px, ld_x = _matrix(x, "x", rows)
-    pw, ld_w = _matrix(weight, "weight", rows, x.dtype)
-    if weight.shape[1] != x.shape[1]:
-        raise ValueError(f"weight: {weight.shape[1]} columns, x has {x.shape[1]}")
-    return LinearArgs(rows=x.shape[0], in_=x.shape[1], out=weight.shape[0], x=px, weight=pw, ld_x=ld_x, ld_weight=ld_w,
-                      dtype=dt)
+    ld_x = _rows_of(x, "x")
+    call = _Call(x)
+    ld_w = _rows_of(weight, "weight", x.dtype)
+    (n, k), (m, k_w) = x.shape, weight.shape
+    if k_w != k:
+        raise ValueError(f"weight: {k_w} columns, x has {k}")
+    if weight.get_device() != call.here:
+        call.odd.append((weight, "weight"))
+    return call, dt, n, k, m, ld_x, ld_w
 
 
 def z1_linear_workspace(x, weight) -> int:
     """Bytes of device workspace z1_linear needs for these operands."""
+    _, dt, n, k, m, ld_x, ld_w = _operands(x, weight)
+    a = LinearArgs(rows=n, in_=k, out=m, x=x.data_ptr(), weight=weight.data_ptr(), ld_x=ld_x, ld_weight=ld_w, dtype=dt)
     b = _I64()
-    _check(lib.z1_linear_workspace(ctypes.byref(_linear_args(x, weight, [])), ctypes.byref(b)), "z1_linear_workspace")
+    _check(lib.z1_linear_workspace(ctypes.byref(a), ctypes.byref(b)), "z1_linear_workspace")
     return b.value
 
 
@@ -180,24 +227,20 @@ def z1_linear(x, weight, y, *, bias=None, act: str = "none", mul=None, residual=
     """y = residual + drop(act(x weight^T + bias) * mul) and pre = x weight^T +
     bias, for x [rows, in], weight [out, in], bias [out] and the others [rows,
     out], all of one type; None leaves a term out.  y may be residual or mul."""
-    items, rows = [], []
-    a = _linear_args(x, weight, rows)
-    shape = (a.rows, a.out)
-    a.y, a.ld_y = _matrix(y, "y", rows, x.dtype, shape)
-    a.mul, a.ld_mul = _matrix(mul, "mul", rows, x.dtype, shape)
-    a.residual, a.ld_residual = _matrix(residual, "residual", rows, x.dtype, shape)
-    a.pre, a.ld_pre = _matrix(pre, "pre", rows, x.dtype, shape)
-    a.act = _act_of(act)
-    if bias is not None:
-        items.append((bias, "bias", x.dtype, a.out))
-        a.bias = _dptr(bias)
-    if dropout is not None:
-        a.drop = _drop_of(dropout, items)
-    n = _bytes_of(workspace)
-    if n:
-        items.append((workspace, "workspace", None, 0))
-    _checked(items, rows)
-    _check(lib.z1_linear(ctypes.byref(a), _dptr(workspace) if n else None, n, _stream(stream)), "z1_linear")
+    call, dt, n, k, m, ld_x, ld_w = _operands(x, weight)
+    kind, shape = x.dtype, (n, m)
+    py, ld_y = call.matrix(y, "y", kind, shape)
+    pm, ld_m = call.matrix(mul, "mul", kind, shape)
+    pr, ld_r = call.matrix(residual, "residual", kind, shape)
+    pp, ld_p = call.matrix(pre, "pre", kind, shape)
+    pb = call.vector(bias, "bias", kind, m)
+    act = _act_of(act)
+    drop = call.dropout(dropout)
+    work, size = call.workspace(workspace)
+    call.done()
+    a = LinearArgs(n, k, m, x.data_ptr(), weight.data_ptr(), pb, pm, pr, pp, py, ld_x, ld_w, ld_m, ld_r, ld_p, ld_y, drop,
+                   dt, act)
+    _check(lib.z1_linear(ctypes.byref(a), work, size, _stream(stream)), "z1_linear")
 
 
 def z1_linear_dz_workspace(rows: int, out: int) -> int:
@@ -214,54 +257,44 @@ def z1_linear_dz(dy, dz=None, *, act: str = "none", pre=None, mul=None, dmul=Non
     dz, dmul and dbias may be None; dz may be dy, pre or mul, dmul may be mul or
     pre."""
     dt = _dtype_of(dy, "dy")
-    items, rows = [], []
-    a = LinearDzArgs(dtype=dt, act=_act_of(act), accumulate=int(bool(accumulate)))
-    a.dy, a.ld_dy = _matrix(dy, "dy", rows)
-    a.rows, a.out = dy.shape
-    for name, t in (("pre", pre), ("mul", mul), ("dz", dz), ("dmul", dmul)):
-        p, ld = _matrix(t, name, rows, dy.dtype, dy.shape)
-        setattr(a, name, p)
-        setattr(a, "ld_" + name, ld)
-    if dbias is not None:
-        items.append((dbias, "dbias", torch.float32, a.out))
-        a.dbias = _dptr(dbias)
-    if dropout is not None:
-        a.drop = _drop_of(dropout, items)
-    n = _bytes_of(workspace)
-    if n:
-        items.append((workspace, "workspace", None, 0))
-    _checked(items, rows)
-    _check(lib.z1_linear_dz(ctypes.byref(a), _dptr(workspace) if n else None, n, _stream(stream)), "z1_linear_dz")
+    ld_dy = _rows_of(dy, "dy")
+    call, kind, shape = _Call(dy), dy.dtype, dy.shape
+    pp, ld_p = call.matrix(pre, "pre", kind, shape)
+    pm, ld_m = call.matrix(mul, "mul", kind, shape)
+    pz, ld_z = call.matrix(dz, "dz", kind, shape)
+    pd, ld_d = call.matrix(dmul, "dmul", kind, shape)
+    pb = call.vector(dbias, "dbias", torch.float32, shape[1])
+    act = _act_of(act)
+    drop = call.dropout(dropout)
+    work, size = call.workspace(workspace)
+    call.done()
+    a = LinearDzArgs(shape[0], shape[1], dy.data_ptr(), pp, pm, pz, pd, pb, ld_dy, ld_p, ld_m, ld_z, ld_d, drop, dt, act,
+                     1 if accumulate else 0, 0)
+    _check(lib.z1_linear_dz(ctypes.byref(a), work, size, _stream(stream)), "z1_linear_dz")
 
 
-def _linear_grad_args(dz, x, weight, dx, dweight, rows: list) -> LinearGradArgs:
-    a = LinearGradArgs(dtype=_dtype_of(dz, "dz"))
-    a.dz, a.ld_dz = _matrix(dz, "dz", rows)
-    n, out = dz.shape
+def _grad_operands(dz, x, weight):
+    """(the call, the arguments without the outputs, the shape of dx, that of dweight)"""
+    dt = _dtype_of(dz, "dz")
+    ld_dz = _rows_of(dz, "dz")
+    call, kind = _Call(dz), dz.dtype
+    n, m = dz.shape
     known = x if x is not None else weight
     if known is None:
         raise ValueError("x and weight: both None")
     _dtype_of(known, "x" if x is not None else "weight")
-    cols = known.shape[-1]
-    a.x, a.ld_x = _matrix(x, "x", rows, dz.dtype, (n, cols))
-    a.weight, a.ld_weight = _matrix(weight, "weight", rows, dz.dtype, (out, cols))
-    a.rows, a.in_, a.out = n, cols, out
-    a.dx, a.ld_dx = _matrix(dx, "dx", rows, dz.dtype, (n, cols))
-    if dweight is not None:
-        a.dweight, a.ld_dweight = _matrix(dweight, "dweight", rows, None, (out, cols))
-        if dweight.dtype != torch.float32 and dweight.dtype != dz.dtype:
-            raise TypeError(f"dweight: dtype {dweight.dtype}, expected float32 or {dz.dtype}")
-        a.dweight_dtype = DTYPES[dweight.dtype]
-    return a
+    k = known.shape[-1]
+    px, ld_x = call.matrix(x, "x", kind, (n, k))
+    pw, ld_w = call.matrix(weight, "weight", kind, (m, k))
+    return call, LinearGradArgs(n, k, m, dz.data_ptr(), px, pw, None, None, None, ld_dz, ld_x, ld_w, 0, 0, 0, dt, 0, 0, 0), (n, k), (m, k)
 
 
 def z1_linear_grad_workspace(dz, x, weight) -> int:
     """Bytes of device workspace z1_linear_grad needs for these operands, for
     either gradient or both."""
-    a = _linear_grad_args(dz, x, weight, None, None, [])
+    a = _grad_operands(dz, x, weight)[1]
     # the outputs are not looked at, but for being there
-    a.dx = a.weight
-    a.dweight = a.x
+    a.dx, a.dweight = a.weight, a.x
     b = _I64()
     _check(lib.z1_linear_grad_workspace(ctypes.byref(a), ctypes.byref(b)), "z1_linear_grad_workspace")
     return b.value
@@ -273,80 +306,94 @@ def z1_linear_grad(dz, x, weight, *, dx=None, add=None, dweight=None, accumulate
     [rows, in] (None without dweight) and weight [out, in] (None without dx).
     dweight: fp32, written or with accumulate added to (for example a view of the
     step's acc arena), or of dz's type and written.  dx may be add."""
-    rows = []
-    a = _linear_grad_args(dz, x, weight, dx, dweight, rows)
+    call, a, like_x, like_w = _grad_operands(dz, x, weight)
+    kind = dz.dtype
     if dx is None and dweight is None:
         raise ValueError("dx and dweight: both None")
-    a.add, a.ld_add = _matrix(add, "add", rows, dz.dtype, (a.rows, a.in_))
-    a.accumulate = int(bool(accumulate))
-    n = _bytes_of(workspace)
-    _checked([(workspace, "workspace", None, 0)] if n else [], rows)
-    _check(lib.z1_linear_grad(ctypes.byref(a), _dptr(workspace) if n else None, n, _stream(stream)), "z1_linear_grad")
+    a.dx, a.ld_dx = call.matrix(dx, "dx", kind, like_x)
+    a.add, a.ld_add = call.matrix(add, "add", kind, like_x)
+    if dweight is not None:
+        to = getattr(dweight, "dtype", None)
+        if to is not torch.float32 and to is not kind:
+            raise TypeError(f"dweight: dtype {to}, expected float32 or {kind}")
+        a.dweight, a.ld_dweight = call.matrix(dweight, "dweight", to, like_w)
+        a.dweight_dtype = DTYPES[to]
+    a.accumulate = 1 if accumulate else 0
+    work, size = call.workspace(workspace)
+    call.done()
+    _check(lib.z1_linear_grad(ctypes.byref(a), work, size, _stream(stream)), "z1_linear_grad")
 
 
 # --------------------------------------------------------------------------
 # queries and keys
 # --------------------------------------------------------------------------
 
-def _heads_of(t, name: str, dtype, shape, rows: list):
+def _heads_of(call, t, name: str, dtype, shape):
     """(address, token stride, head stride) of [tokens, heads, dim] whose heads
     are contiguous and do not overlap; the addresses of no elements are null."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch tensor, got {type(t).__name__}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
     if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     n, h, d = shape
-    rows.append((t, name))
+    if t.get_device() != call.here:
+        call.odd.append((t, name))
     st, sh, sd = t.stride()
-    if d > 1 and sd != 1:
+    if sd != 1 and d > 1:
         raise ValueError(f"{name}: heads not contiguous")
-    sh = sh if h > 1 else d
-    st = st if n > 1 else max(h * sh, d)
+    if h <= 1:
+        sh = d
+    if n <= 1:
+        st = max(h * sh, d)
     # either the heads of a token lie within its stride, or tokens within a head's
     if n * h > 0 and (sh < d or st < d or (st < (h - 1) * sh + d and sh < (n - 1) * st + d)):
         raise ValueError(f"{name}: tokens or heads overlap (strides {st}, {sh} of {d} elements)")
     return t.data_ptr() or None, st, sh
 
 
-def _qk_args(q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved, items, rows, outs, douts):
-    lead = q if q is not None else k
-    if lead is None:
-        lead = next((t for t in outs + (douts or ()) if t is not None), None)
+_NO_HEADS = Heads()
+
+
+def _kind_of_heads(call, name, x, weight, out, dout, dweight, dtype, n, d, grad):
+    """The z1_heads of queries or keys."""
+    shaped = x if x is not None else out
+    if shaped is None:
+        return _NO_HEADS
+    if not isinstance(shaped, torch.Tensor) or shaped.dim() != 3:
+        raise ValueError(f"{name}: expected a 3-D torch tensor (tokens, heads, dim)")
+    shape = (n, shaped.shape[1], d)
+    px = sx = hx = pd = sd = hd = None
+    if x is not None:
+        px, sx, hx = _heads_of(call, x, name, dtype, shape)
+    po, so, ho = _heads_of(call, out, "d" + name if grad else name + "_out", dtype, shape)
+    if grad:
+        pd, sd, hd = _heads_of(call, dout, f"d{name}_out", dtype, shape)
+    return Heads(shape[1], px, po, pd, call.vector(weight, name + "_weight", dtype, d),
+                 call.vector(dweight, f"d{name}_weight", torch.float32, d), sx or 0, hx or 0, so, ho, sd or 0, hd or 0)
+
+
+def _qk_args(q, k, positions, inv_freq, weights, eps, interleaved, outs, douts=(None, None), dweights=(None, None),
+             accumulate=False, grad=False):
+    lead = next((t for t in (q, k) + outs + douts if t is not None), None)
     dt = _dtype_of(lead, "q")
     if lead.dim() != 3:
         raise ValueError(f"q: {lead.dim()} dimensions, expected 3 (tokens, heads, dim)")
+    call, kind = _Call(lead), lead.dtype
     n, _, d = lead.shape
-    a = QkArgs(tokens=n, dim=d, eps=float(eps), dtype=dt, interleaved=int(bool(interleaved)))
-    a.position_type = _itype_of(positions, "positions")
+    it = _itype_of(positions, "positions")
     if positions.shape != (n,):
         raise ValueError(f"positions: shape {tuple(positions.shape)}, expected ({n},)")
-    items.append((positions, "positions", positions.dtype, n))
-    a.positions = positions.data_ptr()
     if not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1:
         raise ValueError("inv_freq: expected a 1-D torch tensor")
-    a.n_freq = inv_freq.numel()
-    items.append((inv_freq, "inv_freq", torch.float64, a.n_freq))
-    a.inv_freq = inv_freq.data_ptr()
-    for i, (name, x, weight, heads) in enumerate((("q", q, q_weight, a.q), ("k", k, k_weight, a.k))):
-        shaped = x if x is not None else outs[i]
-        if shaped is None:
-            continue
-        if not isinstance(shaped, torch.Tensor) or shaped.dim() != 3:
-            raise ValueError(f"{name}: expected a 3-D torch tensor (tokens, heads, dim)")
-        shape = (n, shaped.shape[1], d)
-        heads.heads = shape[1]
-        if x is not None:
-            heads.x, heads.x_token, heads.x_head = _heads_of(x, name, lead.dtype, shape, rows)
-        out = "d" + name if douts else name + "_out"
-        heads.out, heads.out_token, heads.out_head = _heads_of(outs[i], out, lead.dtype, shape, rows)
-        if douts:
-            heads.dout, heads.dout_token, heads.dout_head = _heads_of(douts[i], f"d{name}_out", lead.dtype, shape, rows)
-        if weight is not None:
-            items.append((weight, name + "_weight", lead.dtype, d))
-            heads.weight = _dptr(weight)
-    return a
+    n_freq = inv_freq.numel()
+    a = QkArgs(n, d, n_freq,
+               _kind_of_heads(call, "q", q, weights[0], outs[0], douts[0], dweights[0], kind, n, d, grad),
+               _kind_of_heads(call, "k", k, weights[1], outs[1], douts[1], dweights[1], kind, n, d, grad),
+               call.vector(positions, "positions", positions.dtype, n), call.vector(inv_freq, "inv_freq", torch.float64, n_freq),
+               eps, it, dt, 1 if interleaved else 0, 1 if accumulate else 0)
+    return call, a
 
 
 def z1_qk_norm_rope(q, k, q_out, k_out, positions, inv_freq, *, q_weight=None, k_weight=None, eps: float = 1e-6,
@@ -356,9 +403,8 @@ def z1_qk_norm_rope(q, k, q_out, k_out, positions, inv_freq, *, q_weight=None, k
     2 * len(inv_freq) elements by the angles positions[t] * inv_freq (fp64), into
     q_out and k_out (which may be q and k).  Pairs are halves of the rotated part,
     or neighbours with interleaved.  k and k_out may be None."""
-    items, rows = [], []
-    a = _qk_args(q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved, items, rows, (q_out, k_out), None)
-    _checked(items, rows)
+    call, a = _qk_args(q, k, positions, inv_freq, (q_weight, k_weight), eps, interleaved, (q_out, k_out))
+    call.done()
     _check(lib.z1_qk_norm_rope(ctypes.byref(a), _stream(stream)), "z1_qk_norm_rope")
 
 
@@ -377,17 +423,8 @@ def z1_qk_norm_rope_grad(q, k, dq_out, dk_out, dq, dk, positions, inv_freq, *, q
     outputs, and dq_weight / dk_weight [dim] fp32 (+)= those of the weights (None:
     not wanted).  q, k are the forward's inputs (None where there is no norm);
     dq may be dq_out, dk dk_out."""
-    items, rows = [], []
-    a = _qk_args(q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved, items, rows, (dq, dk),
-                 (dq_out, dk_out))
-    for name, t, heads in (("dq_weight", dq_weight, a.q), ("dk_weight", dk_weight, a.k)):
-        if t is not None:
-            items.append((t, name, torch.float32, a.dim))
-            heads.dweight = _dptr(t)
-    a.accumulate = int(bool(accumulate))
-    n = _bytes_of(workspace)
-    if n:
-        items.append((workspace, "workspace", None, 0))
-    _checked(items, rows)
-    _check(lib.z1_qk_norm_rope_grad(ctypes.byref(a), _dptr(workspace) if n else None, n, _stream(stream)),
-           "z1_qk_norm_rope_grad")
+    call, a = _qk_args(q, k, positions, inv_freq, (q_weight, k_weight), eps, interleaved, (dq, dk), (dq_out, dk_out),
+                       (dq_weight, dk_weight), accumulate, True)
+    work, size = call.workspace(workspace)
+    call.done()
+    _check(lib.z1_qk_norm_rope_grad(ctypes.byref(a), work, size, _stream(stream)), "z1_qk_norm_rope_grad")
