@@ -19,10 +19,11 @@ typedef __attribute__((address_space(3))) void lds_void;
 // LDS as an address space of its own.  The kernels' loops take the ring as two
 // restrict pointers, one that copies write and one that fragments are read from:
 // else the compiler waits for every copy under way before a transposing read.  What
-// orders the two is the kernels' own waits and barriers, each beside a fence that no
-// memory access is moved across.  (The pointers are passed on by value alone, as what
-// a closure holds by reference loses its restrict, and the second one's value is
-// hidden, as a constant argument does too.)
+// orders the two is the kernels' own waits and barriers, each beside a fence that is
+// given both pointers (one that is not is no fence for them: the compiler takes
+// restrict memory that it cannot see passed on for untouched).  The pointers are passed
+// on by value alone, as what a closure holds by reference loses its restrict, and the
+// second one's value is hidden, as a constant argument does too.
 typedef __attribute__((address_space(3))) char lds_char;
 [[maybe_unused]] __device__ __forceinline__ const lds_char *hidden(const lds_char *p)
 {
@@ -30,6 +31,16 @@ typedef __attribute__((address_space(3))) char lds_char;
     asm("" : "+s"(p));
 #endif
     return p;
+}
+
+// The workgroup's barrier, with no access to the ring moved across it.
+[[maybe_unused]] __device__ __forceinline__ void ring_barrier(lds_char *to, const lds_char *from)
+{
+#if defined(__HIP_DEVICE_COMPILE__)
+    asm volatile("" : : "s"(to), "s"(from) : "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" : : "s"(to), "s"(from) : "memory");
+#endif
 }
 
 // acc += A B for the 16 bytes of depth that a lane holds of either operand: one
@@ -370,49 +381,6 @@ __device__ __forceinline__ void multiply(float16v (&acc)[TP][TQ], const uint4v (
             mma(E(), acc[i][j], a[i], b[j]);
 }
 
-// One panel after another, in a ring of RING, so that RING - 1 are on their way while
-// one is multiplied.
-template <typename E, typename SP, typename SQ, int TP, int TQ, int RING>
-__device__ __forceinline__ void ring_loop(lds_char *__restrict__ to, const lds_char *__restrict__ from, SP &sp, SQ &sq,
-                                          const int (&pat)[TP], const int (&qat)[TQ], float16v (&acc)[TP][TQ], int panels,
-                                          int wave)
-{
-    constexpr int kAhead = (RING - 2) * (SP::kLoads + SQ::kLoads);   // copies that may stay out at a wait
-    constexpr int kBytes = SP::kBytes + SQ::kBytes, kParts = SP::kParts;
-#pragma unroll
-    for (int s = 0; s < RING - 1; ++s)
-        if (s < panels) {
-            sp.load(to + s * kBytes, wave);
-            sq.load(to + s * kBytes + SP::kBytes, wave);
-        }
-    int slot = 0;
-    for (int k = 0; k < panels; ++k) {
-        // panel k has arrived, and every wave has read panel k - 1, whose slot the
-        // next copy overwrites
-        if (k + RING - 2 < panels)
-            wait_copies<kAhead>();
-        else
-            wait_copies<0>();
-        asm volatile("" ::: "memory");
-        __builtin_amdgcn_s_barrier();
-        asm volatile("" ::: "memory");
-        if (k + RING - 1 < panels) {
-            const int next = slot == 0 ? RING - 1 : slot - 1;
-            sp.load(to + next * kBytes, wave);
-            sq.load(to + next * kBytes + SP::kBytes, wave);
-        }
-        uint4v a[kParts][TP], b[kParts][TQ];
-        const lds_char *at = from + slot * kBytes;
-#pragma unroll
-        for (int kk = 0; kk < kParts; ++kk)
-            read_part<SP, SQ>(at, at + SP::kBytes, pat, qat, kk, a[kk], b[kk]);
-#pragma unroll
-        for (int kk = 0; kk < kParts; ++kk)
-            multiply<E>(acc, a[kk], b[kk]);
-        slot = slot + 1 == RING ? 0 : slot + 1;
-    }
-}
-
 // What a product's kernel sets up: its tile, its operands' sides, and the places of its
 // wave's fragments; and what it does with its sums.
 template <typename SP, typename SQ, int TILE, int TP, int TQ>
@@ -473,17 +441,19 @@ __device__ __forceinline__ void put_parts(const Product &g, int32_t tp, int32_t 
                     float4v{acc[i][j][4 * r], acc[i][j][4 * r + 1], acc[i][j][4 * r + 2], acc[i][j][4 * r + 3]};
 }
 
-// A wave's sums into C, 32 rows of C at a time through its own part of the LDS, so that
+// A wave's sums into C, up to 64 rows of C at a time through its own part of the LDS, so that
 // TP * 4 lanes write TP * 32 elements of a row together.  Rows are 16 bytes longer than
 // their data, which spreads both accesses over the banks.  What the epilogue reads is
-// fetched kAhead rows early: nothing else hides the wait for it.
+// fetched kAhead rows early, into registers that it is used from: nothing else hides the
+// wait for it, and a copy of them would wait for the stores before it too.
 template <typename OUT, int TILE, int TP, int TQ>
 __device__ __forceinline__ void put_strips(const Product &g, int32_t tp, int32_t tq, int wp, int wq, int wave, int lane,
                                            char *lds, const float16v (&acc)[TP][TQ])
 {
-    constexpr int kRowBytes = TP * 128 + 16, kLanes = TP * 4, kRows = 64 / kLanes, kAhead = 4;
+    constexpr int kRowBytes = TP * 128 + 16, kLanes = TP * 4, kRows = 64 / kLanes;
+    constexpr int kTall = TQ < 2 ? TQ : 2, kAhead = kTall;   // small tiles have other workgroups beside them
     const DropKey key = OUT::kDrops ? drop_key(g.e.drop) : DropKey{};
-    char *own = lds + wave * 32 * kRowBytes;
+    char *own = lds + wave * kTall * 32 * kRowBytes;
     const int half = lane >> 5, low = lane & 31, at = lane % kLanes, row = lane / kLanes;
     const int64_t p0 = (int64_t)tp * TILE + wp * TP * 32 + at * 8, q0 = (int64_t)tq * TILE + wq * TQ * 32 + row;
     const int n = (int)min((int64_t)8, g.P - p0);
@@ -491,41 +461,145 @@ __device__ __forceinline__ void put_strips(const Product &g, int32_t tp, int32_t
     OUT::bias(g.e, (int32_t)p0, n, b);
     typename OUT::In in[kAhead];
     const auto fetch = [&](int r, typename OUT::In &to) {
-        if (n >= 8 && q0 + r < g.Q)
+        if (n >= 8 && q0 + r < g.Q && r < TQ * 32)
             OUT::fetch(g.e, q0 + r, (int32_t)p0, to);
     };
 #pragma unroll
     for (int f = 0; f < kAhead; ++f)
         fetch(f * kRows, in[f]);
 #pragma unroll
-    for (int j = 0; j < TQ; ++j) {
+    for (int j = 0; j < TQ; j += kTall) {
         asm volatile("" ::: "memory");
 #pragma unroll
-        for (int i = 0; i < TP; ++i)
+        for (int k = 0; k < kTall; ++k)
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-                *reinterpret_cast<float4v *>(own + low * kRowBytes + (i * 32 + 8 * r + 4 * half) * 4) =
-                    float4v{acc[i][j][4 * r], acc[i][j][4 * r + 1], acc[i][j][4 * r + 2], acc[i][j][4 * r + 3]};
+            for (int i = 0; i < TP; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    *reinterpret_cast<float4v *>(own + (k * 32 + low) * kRowBytes + (i * 32 + 8 * r + 4 * half) * 4) =
+                        float4v{acc[i][j + k][4 * r], acc[i][j + k][4 * r + 1], acc[i][j + k][4 * r + 2],
+                                acc[i][j + k][4 * r + 3]};
         asm volatile("" ::: "memory");   // a wave's LDS accesses take place in order
 #pragma unroll 1
-        for (int r = 0; r < 32; r += kRows) {
-            const char *from = own + (row + r) * kRowBytes + at * 32;
-            const float4v x = reinterpret_cast<const float4v *>(from)[0], y = reinterpret_cast<const float4v *>(from)[1];
-            float v[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
-            const typename OUT::In now = in[0];
+        for (int r = 0; r < kTall * 32; r += kAhead * kRows)
 #pragma unroll
-            for (int f = 0; f + 1 < kAhead; ++f)
-                in[f] = in[f + 1];
-            if (j * 32 + r + kAhead * kRows < TQ * 32)
-                fetch(j * 32 + r + kAhead * kRows, in[kAhead - 1]);
-            if (n > 0 && q0 + j * 32 + r < g.Q)
-                OUT::put(g.e, key, q0 + j * 32 + r, (int32_t)p0, n, now, b, v);
-        }
+            for (int f = 0; f < kAhead; ++f) {
+                const int64_t q = q0 + j * 32 + r + f * kRows;
+                const char *from = own + (row + r + f * kRows) * kRowBytes + at * 32;
+                const float4v x = reinterpret_cast<const float4v *>(from)[0], y = reinterpret_cast<const float4v *>(from)[1];
+                float v[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+                if (n > 0 && q < g.Q)
+                    OUT::put(g.e, key, q, (int32_t)p0, n, in[f], b, v);
+                fetch(j * 32 + r + (f + kAhead) * kRows, in[f]);
+            }
     }
 }
 
-// One 64 x 64 tile of C, or one piece of its depth.  Several workgroups a compute unit
-// hide each other's waits.
+// A quarter of a panel of k_product_64 and k_product_128: multiplies a0 b0, reads the
+// fragments of part kk of the panel at `at`, and makes the F-th quarter of the wave's
+// copies of a panel on its way to `to`; on 128 tiles in the order P's reads, P's copy,
+// Q's reads, Q's copy, spread between the matrix instructions.  (Reads and copies stay in
+// the order written, as the compiler does not tell a transposing read from what a copy
+// writes.)
+template <typename E, typename SP, typename SQ, int T, int F>
+__device__ __forceinline__ void small_quarter(const lds_char *at, const int (&pat)[T], const int (&qat)[T], int kk,
+                                              uint4v (&a)[T], uint4v (&b)[T], lds_char *to, SP &sp, SQ &sq, int wave,
+                                              float16v (&acc)[T][T], const uint4v (&a0)[T], const uint4v (&b0)[T])
+{
+    static_assert(SP::kLoads == 2 * T && SQ::kLoads == 2 * T && SP::kParts == 4, "the copies of a quarter");
+    constexpr int kMma = sizeof(typename E::store) == 4 ? 4 : 1;   // instructions of an mma
+#pragma unroll
+    for (int i = 0; i < T; ++i)
+        a[i] = SP::frag(at, pat[i], kk);
+    if constexpr (T == 2)
+        sp.template load<F, F + 1>(to, wave);
+    else if constexpr (F < 2)
+        sp.template load<F, F + 1>(to, wave);
+    else
+        sq.template load<F - 2, F - 1>(to + SP::kBytes, wave);
+#pragma unroll
+    for (int j = 0; j < T; ++j)
+        b[j] = SQ::frag(at + SP::kBytes, qat[j], kk);
+    if constexpr (T == 2)
+        sq.template load<F, F + 1>(to + SP::kBytes, wave);
+    multiply<E>(acc, a0, b0);
+    if constexpr (T == 2) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x100, SP::kReads, 0);
+            __builtin_amdgcn_sched_group_barrier(0x008, kMma, 0);
+        }
+        __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x100, SQ::kReads, 0);
+            __builtin_amdgcn_sched_group_barrier(0x008, kMma, 0);
+        }
+        __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+}
+
+// One panel after another in a ring of RING: the fragments of one quarter of a panel's
+// depth are read while the one before is multiplied.  One barrier a panel, in front of
+// its last quarter: behind it every wave has all of panel k in registers, so its slot
+// takes panel k + RING, and panel k + 1 has arrived.  Copies past the last panel bring
+// zeros and keep the count of outstanding ones even.
+template <typename E, typename SP, typename SQ, int T, int RING>
+__device__ __forceinline__ void ahead_loop(lds_char *__restrict__ to, const lds_char *__restrict__ from, SP &sp, SQ &sq,
+                                           const int (&pat)[T], const int (&qat)[T], float16v (&acc)[T][T], int panels, int wave)
+{
+    constexpr int kBytes = SP::kBytes + SQ::kBytes, kCopies = SP::kLoads + SQ::kLoads;
+    uint4v a[2][T], b[2][T];
+    if (panels < RING) {   // all there is fits the ring
+        for (int s = 0; s < panels; ++s) {
+            sp.load(to + s * kBytes, wave);
+            sq.load(to + s * kBytes + SP::kBytes, wave);
+        }
+        wait_copies<0>();
+        ring_barrier(to, from);
+        for (int s = 0; s < panels; ++s)
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+                read_part<SP, SQ>(from + s * kBytes, from + s * kBytes + SP::kBytes, pat, qat, kk, a[0], b[0]);
+                multiply<E>(acc, a[0], b[0]);
+            }
+        return;
+    }
+#pragma unroll
+    for (int s = 0; s < RING - 1; ++s) {
+        sp.load(to + s * kBytes, wave);
+        sq.load(to + s * kBytes + SP::kBytes, wave);
+    }
+    sp.template load<0, 1>(to + (RING - 1) * kBytes, wave);
+    if constexpr (T == 2)
+        sq.template load<0, 1>(to + (RING - 1) * kBytes + SP::kBytes, wave);
+    wait_copies<(RING - 2) * kCopies + T>();
+    ring_barrier(to, from);
+    read_part<SP, SQ>(from, from + SP::kBytes, pat, qat, 0, a[0], b[0]);
+    for (int k = 0; k < panels; k += RING)
+#pragma unroll
+        for (int slot = 0; slot < RING; ++slot) {
+            const lds_char *at = from + slot * kBytes;
+            const int next = slot == RING - 1 ? 0 : slot + 1, before = slot == 0 ? RING - 1 : slot - 1;
+            lds_char *const other = to + before * kBytes;
+            if (k + slot < panels) {
+                small_quarter<E, SP, SQ, T, 1>(at, pat, qat, 1, a[1], b[1], other, sp, sq, wave, acc, a[0], b[0]);
+                small_quarter<E, SP, SQ, T, 2>(at, pat, qat, 2, a[0], b[0], other, sp, sq, wave, acc, a[1], b[1]);
+                small_quarter<E, SP, SQ, T, 3>(at, pat, qat, 3, a[1], b[1], other, sp, sq, wave, acc, a[0], b[0]);
+                __builtin_amdgcn_sched_barrier(0);
+                wait_copies<(RING - 2) * kCopies>();
+                ring_barrier(to, from);
+                __builtin_amdgcn_sched_barrier(0);
+                small_quarter<E, SP, SQ, T, 0>(from + next * kBytes, pat, qat, 0, a[0], b[0], to + slot * kBytes, sp, sq, wave,
+                                               acc, a[1], b[1]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+}
+
+// One 64 x 64 tile of C, or one piece of its depth; up to three workgroups a compute
+// unit.
 template <typename E, bool PD, bool QD, typename OUT>
 __global__ __launch_bounds__(256) void k_product_64(Product g)
 {
@@ -538,94 +612,17 @@ __global__ __launch_bounds__(256) void k_product_64(Product g)
     u.start(g);
     float16v acc[1][1];
     clear(acc);
-    ring_loop<E, SP, SQ, 1, 1, RING>((lds_char *)&lds[0], hidden((const lds_char *)&lds[0]), u.sp, u.sq, u.pat, u.qat, acc,
-                                     u.panels, u.wave);
+    ahead_loop<E, SP, SQ, 1, RING>((lds_char *)&lds[0], hidden((const lds_char *)&lds[0]), u.sp, u.sq, u.pat, u.qat, acc,
+                                   u.panels, u.wave);
     if (g.splits > 1) {
+        wait_copies<0>();   // the LDS is not to be written behind the workgroup's end
         put_parts<TILE>(g, u.tp, u.tq, u.piece, u.wave, u.lane, acc);
         return;
     }
-    const DropKey key = OUT::kDrops ? drop_key(g.e.drop) : DropKey{};
-    float4v v[4];
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-        v[r] = float4v{acc[0][0][4 * r], acc[0][0][4 * r + 1], acc[0][0][4 * r + 2], acc[0][0][4 * r + 3]};
-    put_block<OUT>(g, key, (int64_t)u.tq * TILE + u.wq * 32, (int64_t)u.tp * TILE + u.wp * 32, u.lane, v);
+    wait_copies<0>();   // what still comes must not fall into what the LDS holds next
+    ring_barrier((lds_char *)&lds[0], (const lds_char *)&lds[0]);
+    put_strips<OUT, TILE>(g, u.tp, u.tq, u.wp, u.wq, u.wave, u.lane, &lds[0], acc);
 #endif
-}
-
-// A quarter of a panel of k_product_128: multiplies a0 b0, reads the fragments of part
-// kk of the panel at p and q, and makes the F-th quarter of the wave's copies of a panel
-// on its way to `to`, in the order P's reads, P's copy, Q's reads, Q's copy, spread
-// between the matrix instructions.  (Reads and copies stay in the order written, as the
-// compiler does not tell a transposing read from what a copy writes.)
-template <typename E, typename SP, typename SQ, int F>
-__device__ __forceinline__ void quarter_128(const lds_char *at, const int (&pat)[2], const int (&qat)[2], int kk,
-                                            uint4v (&a)[2], uint4v (&b)[2], lds_char *to, SP &sp, SQ &sq, int wave,
-                                            float16v (&acc)[2][2], const uint4v (&a0)[2], const uint4v (&b0)[2])
-{
-    constexpr int kMma = sizeof(typename E::store) == 4 ? 4 : 1;   // instructions of an mma
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-        a[i] = SP::frag(at, pat[i], kk);
-    sp.template load<F, F + 1>(to, wave);
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-        b[j] = SQ::frag(at + SP::kBytes, qat[j], kk);
-    sq.template load<F, F + 1>(to + SP::kBytes, wave);
-    multiply<E>(acc, a0, b0);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        __builtin_amdgcn_sched_group_barrier(0x100, SP::kReads, 0);
-        __builtin_amdgcn_sched_group_barrier(0x008, kMma, 0);
-    }
-    __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        __builtin_amdgcn_sched_group_barrier(0x100, SQ::kReads, 0);
-        __builtin_amdgcn_sched_group_barrier(0x008, kMma, 0);
-    }
-    __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
-    __builtin_amdgcn_sched_barrier(0);
-}
-
-// As wide_loop below, on a ring of RING panels of both operands.
-template <typename E, typename SP, typename SQ, int RING>
-__device__ __forceinline__ void ahead_loop(lds_char *__restrict__ to, const lds_char *__restrict__ from, SP &sp, SQ &sq,
-                                           const int (&pat)[2], const int (&qat)[2], float16v (&acc)[2][2], int panels, int wave)
-{
-    constexpr int kBytes = SP::kBytes + SQ::kBytes, kCopies = SP::kLoads + SQ::kLoads;
-    static_assert(SP::kLoads == 4 && SQ::kLoads == 4 && SP::kParts == 4, "the schedule below");
-    uint4v a[2][2], b[2][2];
-#pragma unroll
-    for (int s = 0; s < RING - 1; ++s) {
-        sp.load(to + s * kBytes, wave);
-        sq.load(to + s * kBytes + SP::kBytes, wave);
-    }
-    sp.template load<0, 1>(to + (RING - 1) * kBytes, wave);
-    sq.template load<0, 1>(to + (RING - 1) * kBytes + SP::kBytes, wave);
-    wait_copies<(RING - 2) * kCopies + kCopies / 4>();
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-    read_part<SP, SQ>(from, from + SP::kBytes, pat, qat, 0, a[0], b[0]);
-    for (int k = 0; k < panels; k += RING)
-#pragma unroll
-        for (int slot = 0; slot < RING; ++slot) {
-            const lds_char *at = from + slot * kBytes;
-            const int next = slot == RING - 1 ? 0 : slot + 1, before = slot == 0 ? RING - 1 : slot - 1;
-            if (k + slot < panels) {
-                quarter_128<E, SP, SQ, 1>(at, pat, qat, 1, a[1], b[1], to + before * kBytes, sp, sq, wave, acc, a[0], b[0]);
-                quarter_128<E, SP, SQ, 2>(at, pat, qat, 2, a[0], b[0], to + before * kBytes, sp, sq, wave, acc, a[1], b[1]);
-                quarter_128<E, SP, SQ, 3>(at, pat, qat, 3, a[1], b[1], to + before * kBytes, sp, sq, wave, acc, a[0], b[0]);
-                wait_copies<(RING - 2) * kCopies>();
-                asm volatile("" ::: "memory");
-                __builtin_amdgcn_s_barrier();
-                asm volatile("" ::: "memory");
-                __builtin_amdgcn_sched_barrier(0);
-                quarter_128<E, SP, SQ, 0>(from + next * kBytes, pat, qat, 0, a[0], b[0], to + slot * kBytes, sp, sq, wave, acc,
-                                          a[1], b[1]);
-            }
-        }
 }
 
 // One 128 x 128 tile of C, or one piece of its depth, on four waves of 64 x 64.  A
@@ -645,15 +642,14 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
     u.start(g);
     float16v acc[2][2];
     clear(acc);
-    ahead_loop<E, SP, SQ, RING>((lds_char *)&lds[0], hidden((const lds_char *)&lds[0]), u.sp, u.sq, u.pat, u.qat, acc,
-                                u.panels, u.wave);
+    ahead_loop<E, SP, SQ, 2, RING>((lds_char *)&lds[0], hidden((const lds_char *)&lds[0]), u.sp, u.sq, u.pat, u.qat, acc,
+                                   u.panels, u.wave);
     wait_copies<0>();   // what still comes must not fall into what the LDS holds next
     if (g.splits > 1) {
         put_parts<TILE>(g, u.tp, u.tq, u.piece, u.wave, u.lane, acc);
         return;
     }
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
+    ring_barrier((lds_char *)&lds[0], (const lds_char *)&lds[0]);
     put_strips<OUT, TILE>(g, u.tp, u.tq, u.wp, u.wq, u.wave, u.lane, &lds[0], acc);
 #endif
 }
@@ -731,9 +727,7 @@ __device__ __forceinline__ void wide_loop(lds_char *__restrict__ to, const lds_c
     sq.load(to + kQ + SQ::kBytes, wave);
     sp.template load<0, 4>(to + SP::kBytes, wave);
     wait_copies<12>();
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
+    ring_barrier(to, from);
     read_part<SP, SQ>(from, from + kQ, pat, qat, 0, a[0], b[0]);
     int ps = 0, qs = 0;   // the panel's slots
     for (int k = 0; k < panels; ++k) {
@@ -744,9 +738,7 @@ __device__ __forceinline__ void wide_loop(lds_char *__restrict__ to, const lds_c
         quarter<E, SP, SQ, T, 0>(p, q, pat, qat, 2, a[0], b[0], q_free, sq, wave, acc, a[1], b[1]);
         quarter<E, SP, SQ, T, 4>(p, q, pat, qat, 3, a[1], b[1], q_free, sq, wave, acc, a[0], b[0]);
         wait_copies<8>();
-        asm volatile("" ::: "memory");
-        __builtin_amdgcn_s_barrier();
-        asm volatile("" ::: "memory");
+        ring_barrier(to, from);
         __builtin_amdgcn_sched_barrier(0);
         quarter<E, SP, SQ, T, 0>(from + (ps ^ 1) * SP::kBytes, from + kQ + next * SQ::kBytes, pat, qat, 0, a[0], b[0],
                                  to + ps * SP::kBytes, sp, wave, acc, a[1], b[1]);
@@ -773,8 +765,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
         put_parts<TILE>(g, u.tp, u.tq, u.piece, u.wave, u.lane, acc);
         return;
     }
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
+    ring_barrier((lds_char *)&lds[0], (const lds_char *)&lds[0]);
     put_strips<OUT, TILE>(g, u.tp, u.tq, u.wp, u.wq, u.wave, u.lane, &lds[0], acc);
 #endif
 }

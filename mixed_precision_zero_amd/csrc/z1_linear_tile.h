@@ -18,15 +18,17 @@ struct TileChoice {
 };
 
 // The choice with the smallest estimate of its time in microseconds, for a product of
-// P x Q elements and `bytes` of depth, fp32 or 16-bit.  With r = ceil(workgroups / 256)
-// rounds and n panels of 128 bytes a workgroup:
-//   64    4 + 0.55 r + n max(0.26, 0.2 r)     several workgroups share a compute unit
-//   128   2.5 + r (4.3 + 0.46 n)
+// P x Q elements and `bytes` of depth, fp32 or 16-bit.  With t workgroups to each of 256
+// compute units, r = ceil(t) rounds where one takes a unit alone, and n panels of 128
+// bytes a workgroup:
+//   64    3.9 + 0.55 t + n max(0.14 + 0.08 t, 0.175 t)      up to three share a unit
+//   128   2.5 + r (4.3 + n (t < 1 ? 0.33 + 0.15 t : 0.48))
 //   256   r (14 + 1.45 n)
-// and for s pieces a join of 4 + 8 s P Q / 4e6.  fp32 products take 0.45 and 1.75 a
-// panel and round instead, and have no 256 tiles.  Measured (64 / 128 / 256, us, bf16
-// forward): 2048^3 32 / 21.5 / 48, 1024 x 4096 -> 4096 60 / 36 / 81, 2048 x 576 -> 1536
-// 9.0 / 10.2 / 24, 4096^3 206 / 153 / 115, 16384 x 64 -> 4096 50 / 77 / 59.
+// and for s pieces a join of 4 + 8 s P Q / 4e6.  A panel of fp32 takes max(0.54, 0.5 t)
+// and 1.95 r instead, and there are no 256 tiles of it.  Measured (64 / 128 / 256, us,
+// bf16 forward): 2048^3 29 / 22 / 52, 1024 x 4096 -> 4096 55 / 37 / 83, 2048 x 576 -> 1536
+// 9.2 / 11.3 / 29, 1000^3 7.5 / 12.6 / 35, 4096^3 197 / 150 / 117; fp32 1000^3 23 / 67,
+// 2048^3 140 / 140.
 inline TileChoice pick_product(int64_t P, int64_t Q, int64_t bytes, bool fp32)
 {
     TileChoice best{64, 1, 128};
@@ -39,12 +41,12 @@ inline TileChoice pick_product(int64_t P, int64_t Q, int64_t bytes, bool fp32)
         for (int64_t s = 1; s <= 64 && s <= panels; s = s < 4 ? s + 1 : s + s / 2) {
             if (s > 1 && (panels / s < 4 || tiles * s > 1024))
                 break;
-            const double n = (double)((panels + s - 1) / s), r = ceil((double)(tiles * s) / 256.0);
+            const double n = (double)((panels + s - 1) / s), t = (double)(tiles * s) / 256.0, r = ceil(t);
             double cost;
             if (side == 64)
-                cost = 4.0 + 0.55 * r + n * std::max(fp32 ? 0.5 : 0.26, (fp32 ? 0.45 : 0.2) * r);
+                cost = 3.9 + 0.55 * t + n * (fp32 ? std::max(0.54, 0.5 * t) : std::max(0.14 + 0.08 * t, 0.175 * t));
             else if (side == 128)
-                cost = 2.5 + r * (4.3 + (fp32 ? 1.75 : 0.46) * n);
+                cost = 2.5 + r * (4.3 + n * (fp32 ? 1.95 : t < 1.0 ? 0.33 + 0.15 * t : 0.48));
             else
                 cost = r * (14.0 + 1.45 * n);
             if (s > 1)
