@@ -239,32 +239,42 @@ struct Head {
         return i < (which ? nb : na) ? (which ? b : a) + i : -1;
     }
 
-    __device__ __forceinline__ void load(const void *head, float (&x)[2][V]) const
+    // A lane's elements as they lie in memory, and as numbers: apart, so that the
+    // next head's can be on their way while one is worked on.
+    struct Raw {
+        union {
+            Pack16<T> run[2];           // VEC
+            store e[2][V];
+        };
+    };
+    __device__ __forceinline__ void fetch(const void *head, Raw &r) const
     {
         const store *p = static_cast<const store *>(head);
         if (VEC) {
-            Pack16<T> lo, hi;
-            lo.raw = hi.raw = uint4v{0u, 0u, 0u, 0u};
+            r.run[0].raw = r.run[1].raw = uint4v{0u, 0u, 0u, 0u};
             if (na > 0)
-                lo.raw = *reinterpret_cast<const uint4v *>(p + a);
+                r.run[0].raw = *reinterpret_cast<const uint4v *>(p + a);
             if (nb > 0)
-                hi.raw = *reinterpret_cast<const uint4v *>(p + b);
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-#pragma unroll
-                for (int w = 0; w < 2; ++w) {
-                    const int m = INTER ? 2 * i + w : w * V + i;
-                    x[w][i] = T::up(m < V ? lo.e[m % V] : hi.e[m % V]);
-                }
+                r.run[1].raw = *reinterpret_cast<const uint4v *>(p + b);
         } else {
 #pragma unroll
             for (int w = 0; w < 2; ++w)
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
                     const int32_t e = index(w, i);
-                    x[w][i] = e >= 0 ? T::up(p[e]) : 0.f;
+                    r.e[w][i] = e >= 0 ? p[e] : T::down(0.f);
                 }
         }
+    }
+    static __device__ __forceinline__ void values(const Raw &r, float (&x)[2][V])
+    {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+                const int m = VEC && INTER ? 2 * i + w : w * V + i;
+                x[w][i] = T::up(r.e[m / V][m % V]);
+            }
     }
 
     __device__ __forceinline__ void store_to(void *head, const float (&x)[2][V]) const
@@ -300,9 +310,10 @@ constexpr int kQkWaves = 4;
 constexpr int kMostFreq = 256;
 
 struct QkShape {
-    int32_t lanes;        // of a head: a power of two
-    int32_t parts;        // a token's heads are shared out over so many waves
-    int64_t units;        // tokens * parts
+    int32_t lanes;           // of a head: a power of two
+    int32_t groups[2];       // of heads that a wave takes at once: queries, keys
+    int32_t parts[2];        // waves that share the groups of a token; forward: [0], of both kinds
+    uint32_t blocks[2];      // workgroups; forward: [0]
 };
 
 __device__ __forceinline__ int64_t position_of(const z1_qk_args &a, int64_t t)
@@ -311,11 +322,9 @@ __device__ __forceinline__ int64_t position_of(const z1_qk_args &a, int64_t t)
                                      : static_cast<const int64_t *>(a.positions)[t];
 }
 
-// The token's (cos, sin) of every frequency into the wave's LDS, and this lane's
-// V of them out of it.  The angle is reduced to a part of a turn in binary64.
-template <int V>
-__device__ __forceinline__ void turns(const z1_qk_args &a, int64_t t, float2 *lds, int lane, int j, bool pairs,
-                                      float (&cs)[V], float (&sn)[V])
+// The token's (cos, sin) of every frequency into the wave's LDS.  The angle is reduced to
+// a part of a turn in binary64.
+__device__ __forceinline__ void put_turns(const z1_qk_args &a, int64_t t, float2 *lds, int lane)
 {
     const double pos = (double)position_of(a, t);
     asm volatile("" ::: "memory");
@@ -327,22 +336,72 @@ __device__ __forceinline__ void turns(const z1_qk_args &a, int64_t t, float2 *ld
     }
     // one wave's LDS accesses take place in order
     asm volatile("" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const bool there = pairs && j * V + i < a.n_freq;
-        const float2 v = there ? lds[j * V + i] : make_float2(1.f, 0.f);
-        cs[i] = v.x;
-        sn[i] = v.y;
-    }
 }
 
+// (cos, sin) of the lane's i-th pair.
+template <int V>
+__device__ __forceinline__ float2 turn_of(const z1_qk_args &a, const float2 *lds, int j, bool pairs, int i)
+{
+    return pairs && j * V + i < a.n_freq ? lds[j * V + i] : make_float2(1.f, 0.f);
+}
+
+template <int CTRL>
+__device__ __forceinline__ float plus_lane(float x)
+{
+    return x + __uint_as_float(__builtin_amdgcn_mov_dpp(__float_as_uint(x), CTRL, 0xf, 0xf, true));
+}
+
+// The sum over a head's lanes, in all of them: lanes 1 and 2 apart by permutations of
+// four, then mirrors of 8 and 16.
 __device__ __forceinline__ float lane_sum(float x, int lanes)
 {
-    for (int o = lanes >> 1; o > 0; o >>= 1)
-        x += __shfl_xor(x, o);
+    if (lanes > 1)
+        x = plus_lane<0xb1>(x);
+    if (lanes > 2)
+        x = plus_lane<0x4e>(x);
+    if (lanes > 4)
+        x = plus_lane<0x141>(x);
+    if (lanes > 8)
+        x = plus_lane<0x140>(x);
+    if (lanes > 16)
+        x += __shfl_xor(x, 16);
+    if (lanes > 32)
+        x += __shfl_xor(x, 32);
     return x;
 }
 
+// A wave's walk over (token, group of heads).
+struct QkWalk {
+    int64_t unit, units, step, t;
+    int32_t parts, groups, g;
+    bool fresh;              // of a token
+    __device__ __forceinline__ QkWalk(int64_t first, int64_t step_, int64_t tokens, int32_t parts_, int32_t groups_)
+        : unit(first), units(tokens * parts_), step(step_), parts(parts_), groups(groups_), fresh(true)
+    {
+        t = unit / parts;
+        g = (int32_t)(unit % parts);
+    }
+    __device__ __forceinline__ bool here() const { return unit < units; }
+    __device__ __forceinline__ void next()
+    {
+        g += parts;
+        fresh = g >= groups;
+        if (fresh) {
+            unit += step;
+            t = unit / parts;
+            g = (int32_t)(unit % parts);
+        }
+    }
+};
+
+template <typename T>
+__device__ __forceinline__ const typename T::store *head_at(const void *p, int64_t token, int64_t head, int64_t t, int64_t h)
+{
+    return static_cast<const typename T::store *>(p) + t * token + h * head;
+}
+
+// The next group's elements are on their way while one is worked on, and one token's turns
+// stay in registers (8192 tokens of 32 + 32 heads of 128, bf16: 49 us, 5.4 TB/s; 52 without).
 template <typename T, bool VEC, bool INTER>
 __global__ __launch_bounds__(64 * kQkWaves) void k_qk(z1_qk_args a, QkShape sh)
 {
@@ -353,133 +412,151 @@ __global__ __launch_bounds__(64 * kQkWaves) void k_qk(z1_qk_args a, QkShape sh)
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int sub = lane / sh.lanes, across = 64 / sh.lanes;
     const H h(a.dim, a.n_freq, lane % sh.lanes);
-    float wq[2][V], wk[2][V];
+    const float per = 1.f / (float)a.dim, eps = (float)a.eps;
+    typename H::Raw weight[2], raw{};
     if (a.q.weight)
-        h.load(a.q.weight, wq);
+        h.fetch(a.q.weight, weight[0]);
     if (a.k.weight)
-        h.load(a.k.weight, wk);
-    const int64_t q_groups = (a.q.heads + across - 1) / across;
-    for (int64_t unit = (int64_t)blockIdx.x * kQkWaves + wave; unit < sh.units; unit += (int64_t)gridDim.x * kQkWaves) {
-        const int64_t t = unit / sh.parts;
-        const int part = (int)(unit % sh.parts);
-        float cs[V], sn[V];
-        turns<V>(a, t, lds[wave], lane, h.j, h.pairs, cs, sn);
-        const auto kind = [&](const z1_heads &k, const float (&w)[2][V], int64_t first) {
-            for (int64_t g = first; g * across < k.heads; g += sh.parts) {
-                const int64_t head = g * across + sub;
-                const bool there = head < k.heads;
-                float x[2][V];
-                if (there)
-                    h.load(static_cast<const typename T::store *>(k.x) + t * k.x_token + head * k.x_head, x);
-                else
+        h.fetch(a.k.weight, weight[1]);
+    QkWalk w((int64_t)blockIdx.x * kQkWaves + wave, (int64_t)gridDim.x * kQkWaves, a.tokens, sh.parts[0],
+             sh.groups[0] + sh.groups[1]);
+    const auto fetch = [&] {
+        const bool is_k = w.g >= sh.groups[0];
+        const z1_heads &k = is_k ? a.k : a.q;
+        const int64_t head = (int64_t)(w.g - (is_k ? sh.groups[0] : 0)) * across + sub;
+        if (head < k.heads)
+            h.fetch(head_at<T>(k.x, k.x_token, k.x_head, w.t, head), raw);
+        else
+            raw = typename H::Raw{};
+    };
+    if (!w.here())
+        return;
+    fetch();
+    float cs[V], sn[V];
+    while (true) {
+        if (w.fresh) {
+            put_turns(a, w.t, lds[wave], lane);
 #pragma unroll
-                    for (int i = 0; i < V; ++i)
-                        x[0][i] = x[1][i] = 0.f;
-                if (k.weight) {
-                    float s = 0.f;
-#pragma unroll
-                    for (int i = 0; i < V; ++i)
-                        s = fmaf(x[0][i], x[0][i], fmaf(x[1][i], x[1][i], s));
-                    s = lane_sum(s, sh.lanes);
-                    const float inv = rsqrtf(s / (float)a.dim + (float)a.eps);
-#pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        x[0][i] *= inv * w[0][i];
-                        x[1][i] *= inv * w[1][i];
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const float p = x[0][i], q = x[1][i];
-                    x[0][i] = p * cs[i] - q * sn[i];
-                    x[1][i] = q * cs[i] + p * sn[i];
-                }
-                if (there)
-                    h.store_to(static_cast<typename T::store *>(k.out) + t * k.out_token + head * k.out_head, x);
+            for (int i = 0; i < V; ++i) {
+                const float2 turn = turn_of<V>(a, lds[wave], h.j, h.pairs, i);
+                cs[i] = turn.x;
+                sn[i] = turn.y;
             }
-        };
-        kind(a.q, wq, part);
-        // the keys' groups go on where the queries' end
-        kind(a.k, wk, (part + sh.parts - q_groups % sh.parts) % sh.parts);
+        }
+        float x[2][V];
+        H::values(raw, x);
+        const bool is_k = w.g >= sh.groups[0];
+        const z1_heads &k = is_k ? a.k : a.q;
+        const int64_t head = (int64_t)(w.g - (is_k ? sh.groups[0] : 0)) * across + sub, t = w.t;
+        w.next();
+        const bool more = w.here();
+        if (more)
+            fetch();
+        if (k.weight) {
+            float s = 0.f, m[2][V];
+            H::values(is_k ? weight[1] : weight[0], m);
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                s = fmaf(x[0][i], x[0][i], fmaf(x[1][i], x[1][i], s));
+            const float inv = rsqrtf(fmaf(lane_sum(s, sh.lanes), per, eps));
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                x[0][i] *= inv * m[0][i];
+                x[1][i] *= inv * m[1][i];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const float p = x[0][i], q = x[1][i];
+            x[0][i] = fmaf(p, cs[i], -(q * sn[i]));
+            x[1][i] = fmaf(q, cs[i], p * sn[i]);
+        }
+        if (head < k.heads)
+            h.store_to(const_cast<typename T::store *>(head_at<T>(k.out, k.out_token, k.out_head, t, head)), x);
+        if (!more)
+            return;
     }
 }
 
 // The gradient.  With g the output's gradient turned back, xh = x / norm:
 //   dw = sum g xh,   dx = (g w - xh mean(g w xh)) / norm
-// both means from one pass over the head.  The waves walk the tokens a grid
-// apart and keep dw in registers.
+// both means from one pass over the head.  A workgroup takes queries or keys alone, so
+// that a wave holds one weight and one dw, and takes cosines and sines from LDS each
+// time: four waves a SIMD, all 1024 workgroups at once.  8192 tokens of 32 + 32 heads of
+// 128, bf16: 91 us, 53 without norm; with the turns in registers and the next heads'
+// elements fetched ahead, three waves a SIMD, 91 and 59; with both weights in every wave,
+// two a SIMD, 108 and 67.  Memory bounds it without norm (268 MB at 5.1 TB/s); with norm
+// 402 MB at 4.5 TB/s, then the join, with the lanes' sums between.
 template <typename T, bool VEC, bool INTER>
 __global__ __launch_bounds__(64 * kQkWaves) void k_qk_grad(z1_qk_args a, QkShape sh, float *parts)
 {
     typedef Head<T, VEC, INTER> H;
     constexpr int V = H::V;
     __shared__ float2 lds[kQkWaves][kMostFreq];
-    __shared__ float sums[kQkWaves][2][512];
+    __shared__ float sums[kQkWaves][512];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int sub = lane / sh.lanes, across = 64 / sh.lanes;
+    const int is_k = blockIdx.x >= sh.blocks[0];
+    const z1_heads &k = is_k ? a.k : a.q;
+    const uint32_t block = blockIdx.x - (is_k ? sh.blocks[0] : 0);
     const H h(a.dim, a.n_freq, lane % sh.lanes);
-    float wq[2][V], wk[2][V], dq[2][V], dk[2][V];
-    if (a.q.weight)
-        h.load(a.q.weight, wq);
-    if (a.k.weight)
-        h.load(a.k.weight, wk);
+    const float per = 1.f / (float)a.dim, eps = (float)a.eps;
+    float dw[2][V];
 #pragma unroll
     for (int i = 0; i < V; ++i)
-        dq[0][i] = dq[1][i] = dk[0][i] = dk[1][i] = 0.f;
-    const int64_t q_groups = (a.q.heads + across - 1) / across;
-    for (int64_t unit = (int64_t)blockIdx.x * kQkWaves + wave; unit < sh.units; unit += (int64_t)gridDim.x * kQkWaves) {
-        const int64_t t = unit / sh.parts;
-        const int part = (int)(unit % sh.parts);
-        float cs[V], sn[V];
-        turns<V>(a, t, lds[wave], lane, h.j, h.pairs, cs, sn);
-        const auto kind = [&](const z1_heads &k, const float (&w)[2][V], float (&dw)[2][V], int64_t first) {
-            for (int64_t g = first; g * across < k.heads; g += sh.parts) {
-                const int64_t head = g * across + sub;
-                const bool there = head < k.heads;
-                float x[2][V], d[2][V];
+        dw[0][i] = dw[1][i] = 0.f;
+    typename H::Raw weight{};
+    const bool norm = k.weight != nullptr;
+    if (norm)
+        h.fetch(k.weight, weight);
+    for (QkWalk w((int64_t)block * kQkWaves + wave, (int64_t)sh.blocks[is_k] * kQkWaves, a.tokens, sh.parts[is_k],
+                  sh.groups[is_k]);
+         w.here(); w.next()) {
+        if (w.fresh)
+            put_turns(a, w.t, lds[wave], lane);
+        const int64_t head = (int64_t)w.g * across + sub;
+        const bool there = head < k.heads;
+        typename H::Raw rx{}, rd{};
+        if (there) {
+            h.fetch(head_at<T>(k.dout, k.dout_token, k.dout_head, w.t, head), rd);
+            if (norm)
+                h.fetch(head_at<T>(k.x, k.x_token, k.x_head, w.t, head), rx);
+        }
+        float x[2][V], d[2][V];
+        H::values(rd, d);
+        H::values(rx, x);
 #pragma unroll
-                for (int i = 0; i < V; ++i)
-                    x[0][i] = x[1][i] = d[0][i] = d[1][i] = 0.f;
-                if (there) {
-                    h.load(static_cast<const typename T::store *>(k.dout) + t * k.dout_token + head * k.dout_head, d);
-                    if (k.weight)
-                        h.load(static_cast<const typename T::store *>(k.x) + t * k.x_token + head * k.x_head, x);
-                }
+        for (int i = 0; i < V; ++i) {
+            const float2 turn = turn_of<V>(a, lds[wave], h.j, h.pairs, i);
+            const float p = d[0][i], q = d[1][i];
+            d[0][i] = fmaf(p, turn.x, q * turn.y);
+            d[1][i] = fmaf(q, turn.x, -(p * turn.y));
+        }
+        if (norm) {
+            float s = 0.f, m = 0.f, g[2][V];
+            H::values(weight, g);
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    const float p = d[0][i], q = d[1][i];
-                    d[0][i] = p * cs[i] + q * sn[i];
-                    d[1][i] = q * cs[i] - p * sn[i];
+                    g[q][i] *= d[q][i];
+                    s = fmaf(x[q][i], x[q][i], s);
+                    m = fmaf(g[q][i], x[q][i], m);
                 }
-                if (k.weight) {
-                    float s = 0.f, m = 0.f;
+            // a head that is not there has no norm either (eps may be 0)
+            const float inv = there ? rsqrtf(fmaf(lane_sum(s, sh.lanes), per, eps)) : 0.f;
+            const float pull = lane_sum(m, sh.lanes) * per * inv * inv * inv;
 #pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        s = fmaf(x[0][i], x[0][i], fmaf(x[1][i], x[1][i], s));
-                        m = fmaf(d[0][i] * w[0][i], x[0][i], fmaf(d[1][i] * w[1][i], x[1][i], m));
-                    }
-                    s = lane_sum(s, sh.lanes);
-                    m = lane_sum(m, sh.lanes);
-                    const float inv = rsqrtf(s / (float)a.dim + (float)a.eps);
-                    const float mean = m * inv / (float)a.dim;
-                    const bool counts = there;   // a head that is not there has no norm either (eps may be 0)
+            for (int q = 0; q < 2; ++q)
 #pragma unroll
-                    for (int q = 0; q < 2; ++q)
-#pragma unroll
-                        for (int i = 0; i < V; ++i) {
-                            const float xh = x[q][i] * inv;
-                            if (counts)
-                                dw[q][i] = fmaf(d[q][i], xh, dw[q][i]);
-                            d[q][i] = inv * fmaf(-xh, mean, d[q][i] * w[q][i]);
-                        }
+                for (int i = 0; i < V; ++i) {
+                    dw[q][i] = fmaf(d[q][i], x[q][i] * inv, dw[q][i]);
+                    d[q][i] = fmaf(-x[q][i], pull, g[q][i] * inv);
                 }
-                if (there)
-                    h.store_to(static_cast<typename T::store *>(k.out) + t * k.out_token + head * k.out_head, d);
-            }
-        };
-        kind(a.q, wq, dq, part);
-        kind(a.k, wk, dk, (part + sh.parts - q_groups % sh.parts) % sh.parts);
+        }
+        if (there)
+            h.store_to(const_cast<typename T::store *>(head_at<T>(k.out, k.out_token, k.out_head, w.t, head)), d);
     }
     if (!parts)
         return;
@@ -487,25 +564,46 @@ __global__ __launch_bounds__(64 * kQkWaves) void k_qk_grad(z1_qk_args a, QkShape
     for (int q = 0; q < 2; ++q)
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            float x = dq[q][i], y = dk[q][i];
-            for (int o = sh.lanes; o < 64; o <<= 1) {
+            float x = dw[q][i];
+            for (int o = sh.lanes; o < 64; o <<= 1)
                 x += __shfl_xor(x, o);
-                y += __shfl_xor(y, o);
-            }
             const int32_t e = h.index(q, i);
-            if (sub == 0 && e >= 0) {
-                sums[wave][0][e] = x;
-                sums[wave][1][e] = y;
-            }
+            if (sub == 0 && e >= 0)
+                sums[wave][e] = x;
         }
     __syncthreads();
-    for (int i = threadIdx.x; i < 2 * a.dim; i += 64 * kQkWaves) {
-        const int q = i / a.dim, e = i % a.dim;
-        float s = sums[0][q][e];
+    for (int e = threadIdx.x; e < a.dim; e += 64 * kQkWaves) {
+        float s = sums[0][e];
 #pragma unroll
-        for (int w = 1; w < kQkWaves; ++w)
-            s += sums[w][q][e];
-        parts[(int64_t)blockIdx.x * 2 * a.dim + i] = s;
+        for (int w2 = 1; w2 < kQkWaves; ++w2)
+            s += sums[w2][e];
+        parts[(int64_t)blockIdx.x * a.dim + e] = s;
+    }
+}
+
+// Either dweight (+)= the sum of its workgroups' rows of parts: as k_join, blockIdx.y 0
+// for queries and 1 for keys.
+__global__ __launch_bounds__(1024) void k_qk_join(const float *parts, z1_qk_args a, QkShape sh)
+{
+    __shared__ float lds[16][64];
+    const int cx = threadIdx.x & 63, rx = threadIdx.x >> 6, is_k = blockIdx.y;
+    float *out = is_k ? a.k.dweight : a.q.dweight;
+    if (!out)
+        return;
+    const float *from = parts + (is_k ? (int64_t)sh.blocks[0] * a.dim : 0);
+    const int64_t c = blockIdx.x * 64ll + cx;
+    float s = 0.f;
+    if (c < a.dim)
+#pragma unroll 8
+        for (uint32_t r = rx; r < sh.blocks[is_k]; r += 16)
+            s += from[(int64_t)r * a.dim + c];
+    lds[rx][cx] = s;
+    __syncthreads();
+    if (rx == 0 && c < a.dim) {
+#pragma unroll
+        for (int q = 1; q < 16; ++q)
+            s += lds[q][cx];
+        out[c] = a.accumulate ? out[c] + s : s;
     }
 }
 
@@ -536,35 +634,42 @@ bool qk_vec(const z1_qk_args &a, bool grad)
     return true;
 }
 
-QkShape qk_shape(const z1_qk_args &a, int chunks)
+QkShape qk_shape(const z1_qk_args &a, int chunks, bool grad)
 {
     QkShape s{};
     s.lanes = 1;
     while (s.lanes < chunks)
         s.lanes <<= 1;
     const int64_t across = 64 / s.lanes;
-    const int64_t groups = (a.q.heads + across - 1) / across + (a.k.heads + across - 1) / across;
+    const int64_t heads[2] = {a.q.heads, a.k.heads};
+    for (int i = 0; i < 2; ++i)
+        s.groups[i] = (int32_t)((heads[i] + across - 1) / across);
     // few tokens: several waves share one, down to one group of heads each
-    s.parts = (int32_t)std::max<int64_t>(1, std::min<int64_t>(groups, 2048 / std::max<int64_t>(1, a.tokens)));
-    s.units = a.tokens * s.parts;
+    const int64_t most = 2048 / std::max<int64_t>(1, a.tokens);
+    const auto parts = [&](int64_t groups) { return (int32_t)std::max<int64_t>(1, std::min<int64_t>(groups, most)); };
+    if (!grad) {
+        s.parts[0] = parts(s.groups[0] + s.groups[1]);
+        s.blocks[0] = (uint32_t)std::min<int64_t>(8192, (a.tokens * s.parts[0] + kQkWaves - 1) / kQkWaves);
+        return s;
+    }
+    for (int i = 0; i < 2; ++i) {
+        s.parts[i] = parts(s.groups[i]);
+        s.blocks[i] = (uint32_t)qk_grad_groups(a.tokens, a.q.heads, a.k.heads, i);
+    }
     return s;
 }
 
 template <typename T, bool VEC, bool INTER>
 hipError_t qk_run(const z1_qk_args &a, float *parts, bool grad, hipStream_t s)
 {
-    const QkShape sh = qk_shape(a, Head<T, VEC, INTER>::chunks(a.dim, a.n_freq));
-    const int64_t groups = qk_grad_groups(a.tokens, a.q.heads + a.k.heads);
-    if (!grad)
-        k_qk<T, VEC, INTER><<<(uint32_t)std::min<int64_t>(8192, (sh.units + kQkWaves - 1) / kQkWaves), 64 * kQkWaves, 0, s>>>(a, sh);
-    else
-        k_qk_grad<T, VEC, INTER><<<(uint32_t)groups, 64 * kQkWaves, 0, s>>>(a, sh, parts);
-    if (grad && parts) {
-        const uint32_t grid = (uint32_t)((a.dim + 63) / 64);
-        if (a.q.dweight)
-            k_join<<<grid, 1024, 0, s>>>(parts, groups, a.dim, 2 * a.dim, a.q.dweight, a.accumulate);
-        if (a.k.dweight)
-            k_join<<<grid, 1024, 0, s>>>(parts + a.dim, groups, a.dim, 2 * a.dim, a.k.dweight, a.accumulate);
+    const QkShape sh = qk_shape(a, Head<T, VEC, INTER>::chunks(a.dim, a.n_freq), grad);
+    if (!grad) {
+        k_qk<T, VEC, INTER><<<sh.blocks[0], 64 * kQkWaves, 0, s>>>(a, sh);
+    } else {
+        if (sh.blocks[0] + sh.blocks[1] > 0)
+            k_qk_grad<T, VEC, INTER><<<sh.blocks[0] + sh.blocks[1], 64 * kQkWaves, 0, s>>>(a, sh, parts);
+        if (a.q.dweight || a.k.dweight)   // of no tokens: written as zeros from no parts
+            k_qk_join<<<dim3((uint32_t)((a.dim + 63) / 64), 2), 1024, 0, s>>>(parts, a, sh);
     }
     return hipGetLastError();
 }
@@ -616,11 +721,15 @@ hipError_t launch_linear_dz(const z1_linear_dz_args &a, const Drop &d, float *pa
     return hipGetLastError();
 }
 
-int64_t qk_grad_groups(int64_t tokens, int64_t heads)
+int64_t qk_grad_groups(int64_t tokens, int64_t q_heads, int64_t k_heads, int kind)
 {
-    // enough waves for every token, and for few tokens' heads, up to four
-    // workgroups a compute unit
-    return std::max<int64_t>(1, std::min<int64_t>(1024, (tokens * std::min<int64_t>(heads, 64) + kQkWaves - 1) / kQkWaves));
+    // enough waves for every token, and for few tokens' heads, up to four workgroups a
+    // compute unit, shared out by the heads
+    const int64_t heads = kind ? k_heads : q_heads, both = q_heads + k_heads;
+    if (heads == 0 || tokens == 0)
+        return 0;
+    const int64_t wanted = (tokens * std::min<int64_t>(heads, 64) + kQkWaves - 1) / kQkWaves;
+    return std::max<int64_t>(1, std::min<int64_t>(1024 * heads / both, wanted));
 }
 
 hipError_t launch_qk(const z1_qk_args &a, hipStream_t s)

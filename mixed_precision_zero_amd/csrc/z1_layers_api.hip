@@ -387,7 +387,7 @@ z1_status z1_qk_norm_rope_grad_workspace(int64_t tokens, int64_t q_heads, int64_
     if (!bytes || tokens < 0 || tokens > INT32_MAX || q_heads < 0 || q_heads > (1 << 16) || k_heads < 0 ||
         k_heads > (1 << 16) || dim < 1 || dim > 512)
         return Z1_EINVAL;
-    *bytes = z1::ops::qk_grad_groups(tokens, q_heads + k_heads) * 2 * dim * 4;
+    *bytes = (z1::ops::qk_grad_groups(tokens, q_heads, k_heads, 0) + z1::ops::qk_grad_groups(tokens, q_heads, k_heads, 1)) * dim * 4;
     return Z1_OK;
 }
 

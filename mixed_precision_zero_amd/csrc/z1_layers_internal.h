@@ -276,9 +276,9 @@ inline int64_t dz_piece(int64_t rows, int64_t out)
 }
 hipError_t launch_linear_dz(const z1_linear_dz_args &a, const Drop &d, float *parts, hipStream_t s);
 
-// Workgroups of z1_qk_norm_rope_grad, each of which leaves a row of sums for
-// either weight.
-int64_t qk_grad_groups(int64_t tokens, int64_t heads);
+// Workgroups that z1_qk_norm_rope_grad gives to queries (kind 0) or keys (1), each of
+// which leaves a row of sums.
+int64_t qk_grad_groups(int64_t tokens, int64_t q_heads, int64_t k_heads, int kind);
 hipError_t launch_qk(const z1_qk_args &a, hipStream_t s);
 hipError_t launch_qk_grad(const z1_qk_args &a, float *parts, hipStream_t s);
 
