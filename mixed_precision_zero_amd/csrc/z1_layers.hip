@@ -81,7 +81,8 @@ __global__ __launch_bounds__(256) void k_dropout(z1_dropout_args a, Drop d)
 // columns: LX lanes of eight columns, 256 / LX of rows; the column sums of its piece go
 // to a row of `parts`, which k_join adds up.  The pieces are as small as 1024 workgroups
 // make them (2048 x 1536 with SILU and a product, bf16: 29 us in pieces of 64 rows, 192
-// workgroups; X in pieces of 16).
+// workgroups; 9.8 in pieces of 16: 31 MB at 3.2 TB/s, at which size the launch is half
+// of it).
 // --------------------------------------------------------------------------
 template <typename T, int LX>
 __global__ __launch_bounds__(256) void k_linear_dz(z1_linear_dz_args a, Drop d, float *parts, int64_t piece)
@@ -483,9 +484,9 @@ __global__ __launch_bounds__(64 * kQkWaves) void k_qk(z1_qk_args a, QkShape sh)
 // both means from one pass over the head.  A workgroup takes queries or keys alone, so
 // that a wave holds one weight and one dw, and takes cosines and sines from LDS each
 // time: four waves a SIMD, all 1024 workgroups at once.  8192 tokens of 32 + 32 heads of
-// 128, bf16: 91 us, 53 without norm; with the turns in registers and the next heads'
+// 128, bf16: 91 us, 50 without norm; with the turns in registers and the next heads'
 // elements fetched ahead, three waves a SIMD, 91 and 59; with both weights in every wave,
-// two a SIMD, 108 and 67.  Memory bounds it without norm (268 MB at 5.1 TB/s); with norm
+// two a SIMD, 108 and 67.  Memory bounds it without norm (268 MB at 5.4 TB/s); with norm
 // 402 MB at 4.5 TB/s, then the join, with the lanes' sums between.
 template <typename T, bool VEC, bool INTER>
 __global__ __launch_bounds__(64 * kQkWaves) void k_qk_grad(z1_qk_args a, QkShape sh, float *parts)
@@ -513,8 +514,6 @@ __global__ __launch_bounds__(64 * kQkWaves) void k_qk_grad(z1_qk_args a, QkShape
     for (QkWalk w((int64_t)block * kQkWaves + wave, (int64_t)sh.blocks[is_k] * kQkWaves, a.tokens, sh.parts[is_k],
                   sh.groups[is_k]);
          w.here(); w.next()) {
-        if (w.fresh)
-            put_turns(a, w.t, lds[wave], lane);
         const int64_t head = (int64_t)w.g * across + sub;
         const bool there = head < k.heads;
         typename H::Raw rx{}, rd{};
@@ -523,6 +522,8 @@ __global__ __launch_bounds__(64 * kQkWaves) void k_qk_grad(z1_qk_args a, QkShape
             if (norm)
                 h.fetch(head_at<T>(k.x, k.x_token, k.x_head, w.t, head), rx);
         }
+        if (w.fresh)
+            put_turns(a, w.t, lds[wave], lane);
         float x[2][V], d[2][V];
         H::values(rd, d);
         H::values(rx, x);

@@ -714,7 +714,8 @@ __device__ __forceinline__ void quarter(const lds_char *p, const lds_char *q, co
 // and a wave that has to wait for it issues no matrix instruction either.  Copies past
 // the last panel bring zeros and keep the count of outstanding ones even.
 // 8192^3, us: with 64-byte panels, whose deep rows are half a cache line, and all of a
-// panel's copies behind its barrier 904, spread over the panel 899.
+// panel's copies behind its barrier 904, spread over the panel 899; as it is 794 (1.38
+// PFLOP/s).
 template <typename E, typename SP, typename SQ, int T>
 __device__ __forceinline__ void wide_loop(lds_char *__restrict__ to, const lds_char *__restrict__ from, SP &sp, SQ &sq,
                                           const int (&pat)[T], const int (&qat)[T], float16v (&acc)[T][T], int panels, int wave)
@@ -833,8 +834,8 @@ hipError_t product_of(Form form, int32_t out_dtype, const Product &g, hipStream_
 // z1_linear of up to R rows: the weight is read once and everything else is small, so a
 // wave streams two rows of it past x, each lane its groups of eight elements, and the
 // lanes' sums are added up; eight outputs a workgroup go through the epilogue together.
-// Operands at any alignment.  1 x 2048 -> 2048 bf16: 3.x us (split products of 64 tiles
-// and their join 10).
+// Operands at any alignment.  1 x 2048 -> 2048 bf16: 4.4 us (split products of 64
+// tiles and their join 10).  Memory bounds it: 1 x 4096 -> 11008 reads its weight at 4.4 TB/s.
 template <typename E, int R, typename OUT>
 __global__ __launch_bounds__(256) void k_linear_rows(Product g)
 {
