@@ -26,7 +26,8 @@
  * distance.
  *
  * Errors of every call: Z1_EINVAL for null pointers, sizes, types, values that
- * are not finite, a workspace that is too small, a stream of another GPU;
+ * are not finite, a workspace that is too small, a stream of another GPU, an
+ * output that is another buffer of the call at the same address and may not be;
  * Z1_EALIGN for a misaligned pointer; Z1_EHIP for a failed launch.
  */
 #ifndef Z1_LAYERS_H
@@ -113,7 +114,8 @@ typedef struct z1_linear_args {
 /* Bytes of device workspace the call needs for these sizes, row distances and
  * alignments of x and weight (0 for many, and for up to 4 rows): copies of
  * operands whose rows are not 16-byte aligned throughout, and partial sums where
- * a deep product of few tiles is split.  Only sizes, dtype, x, weight and their distances are read. */
+ * a deep product of few tiles is split.  Only sizes, dtype, x, weight and their
+ * distances are read. */
 z1_status z1_linear_workspace(const z1_linear_args *args, int64_t *bytes);
 
 /* workspace: 16-byte aligned, may be NULL where no byte is needed. */
@@ -217,7 +219,8 @@ typedef struct z1_qk_args {
 z1_status z1_qk_norm_rope(const z1_qk_args *args, z1_stream stream);
 
 /* d input = the gradient through rotation and norm (out may be dout with the
- * same strides); dweight (+)= its sum over tokens and heads in fp32. */
+ * same strides); dweight (+)= its sum over tokens and heads in fp32.  Queries and
+ * keys have dweights of their own, also where they share a weight. */
 z1_status z1_qk_norm_rope_grad_workspace(int64_t tokens, int64_t q_heads, int64_t k_heads,
                                          int32_t dim, int64_t *bytes);
 z1_status z1_qk_norm_rope_grad(const z1_qk_args *args, void *workspace, int64_t workspace_bytes,

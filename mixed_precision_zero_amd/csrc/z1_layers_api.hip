@@ -2,6 +2,7 @@
 // include/z1_layers.h: argument validation, the shapes of the products and of
 // their workspaces, and the launches.
 #include <algorithm>
+#include <initializer_list>
 
 #include "z1_host.h"
 #include "z1_layers.h"
@@ -37,6 +38,12 @@ bool rows_ok(const void *p, int64_t rows, int64_t cols, int64_t ld, bool needed)
     if (!p)
         return !needed || rows == 0;
     return ld >= cols;
+}
+
+// Whether one of the others is this buffer.
+bool among(const void *p, std::initializer_list<const void *> others)
+{
+    return p && std::find(others.begin(), others.end(), p) != others.end();
 }
 
 // --------------------------------------------------------------------------
@@ -198,7 +205,12 @@ bool heads_ok(const z1_heads &k, int64_t tokens, bool grad)
         return false;
     if (k.heads == 0 || tokens == 0)
         return true;
-    return k.out && (!grad || k.dout) && (k.x || (grad && !k.weight));
+    // out may be the input (or in the gradient dout) with the same strides
+    const auto apart = [&](const void *p, int64_t token, int64_t head) {
+        return p != k.out || ((tokens == 1 || token == k.out_token) && (k.heads == 1 || head == k.out_head));
+    };
+    return k.out && (!grad || k.dout) && (k.x || (grad && !k.weight)) && apart(k.x, k.x_token, k.x_head) &&
+           (!grad || apart(k.dout, k.dout_token, k.dout_head));
 }
 
 z1_status qk_check(const z1_qk_args *a, bool grad)
@@ -210,7 +222,10 @@ z1_status qk_check(const z1_qk_args *a, bool grad)
         return Z1_EINVAL;
     if ((a->tokens > 0 && !a->positions) || (a->n_freq > 0 && !a->inv_freq))
         return Z1_EINVAL;
-    if (grad && ((a->q.dweight && !a->q.weight) || (a->k.dweight && !a->k.weight)))
+    if (grad && ((a->q.dweight && !a->q.weight) || (a->k.dweight && !a->k.weight) || among(a->q.dweight, {a->k.dweight})))
+        return Z1_EINVAL;
+    if (a->tokens > 0 && a->q.heads > 0 && a->k.heads > 0 &&
+        (among(a->q.out, {a->k.out, a->k.x, grad ? a->k.dout : nullptr}) || among(a->k.out, {a->q.x, grad ? a->q.dout : nullptr})))
         return Z1_EINVAL;
     const size_t size = type_size(a->dtype);
     for (const z1_heads *k : {&a->q, &a->k})
@@ -261,6 +276,9 @@ z1_status z1_linear(const z1_linear_args *a, void *workspace, int64_t workspace_
         !rows_ok(a->mul, a->rows, a->out, a->ld_mul, false) || !rows_ok(a->residual, a->rows, a->out, a->ld_residual, false))
         return Z1_EINVAL;
     if (a->rows > 1 && ((a->y == a->residual && a->ld_y != a->ld_residual) || (a->y == a->mul && a->ld_y != a->ld_mul)))
+        return Z1_EINVAL;
+    if (a->rows > 0 && (among(a->y, {a->x, a->weight, a->bias, a->pre}) ||
+                        among(a->pre, {a->x, a->weight, a->bias, a->mul, a->residual})))
         return Z1_EINVAL;
     const z1_status ws = workspace_ok(workspace, workspace_bytes, w.bytes);
     if (ws == Z1_EINVAL)
@@ -344,6 +362,10 @@ z1_status z1_linear_grad(const z1_linear_grad_args *a, void *workspace, int64_t 
         (a->dweight && a->ld_dweight < a->in))
         return Z1_EINVAL;
     if (a->rows > 1 && a->dx && a->dx == a->add && a->ld_dx != a->ld_add)
+        return Z1_EINVAL;
+    // dx is written before dweight is computed; without dweight x is not read
+    if (a->rows > 0 && (among(a->dx, {a->dz, a->weight, a->dweight, a->dweight ? a->x : nullptr}) ||
+                        among(a->dweight, {a->dz, a->x, a->dx ? a->weight : nullptr, a->dx ? a->add : nullptr})))
         return Z1_EINVAL;
     const z1_status ws = workspace_ok(workspace, workspace_bytes, w.bytes);
     if (ws == Z1_EINVAL)

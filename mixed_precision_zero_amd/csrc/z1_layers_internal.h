@@ -179,7 +179,8 @@ __device__ __forceinline__ float act_slope(float z)
         return fmaf(z * 0.39894228040143268f, expf(-0.5f * z * z), 0.5f * erfcf(z * -0.70710678118654752f));
     if constexpr (ACT == Z1_ACT_GELU_TANH) {
         const float s = sigmoid(gelu_tanh_arg(z));
-        return fmaf(z * s * (1.f - s), 1.5957691216057308f * fmaf(3.f * 0.044715f * z, z, 1.f), s);
+        // s (1 - s) is 0 long before z^2 is infinite
+        return fmaf(z * s * (1.f - s), 1.5957691216057308f * fmaf(3.f * 0.044715f, fminf(z * z, 1e30f), 1.f), s);
     }
     if constexpr (ACT == Z1_ACT_SILU) {
         const float s = sigmoid(z);

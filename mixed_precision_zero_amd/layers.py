@@ -421,8 +421,8 @@ def z1_qk_norm_rope_grad(q, k, dq_out, dk_out, dq, dk, positions, inv_freq, *, q
                          accumulate: bool = False, workspace=None, stream=None) -> None:
     """dq and dk from the gradients dq_out and dk_out of z1_qk_norm_rope's
     outputs, and dq_weight / dk_weight [dim] fp32 (+)= those of the weights (None:
-    not wanted).  q, k are the forward's inputs (None where there is no norm);
-    dq may be dq_out, dk dk_out."""
+    not wanted; two buffers, also for a weight that both share).  q, k are the
+    forward's inputs (None where there is no norm); dq may be dq_out, dk dk_out."""
     call, a = _qk_args(q, k, positions, inv_freq, (q_weight, k_weight), eps, interleaved, (dq, dk), (dq_out, dk_out),
                        (dq_weight, dk_weight), accumulate, True)
     work, size = call.workspace(workspace)

@@ -381,3 +381,17 @@ def test_captured_step_draws_new_masks():
         assert last is None or not torch.equal(last, held["y"])
         last = held["y"].clone()
         assert state.tolist() == [11, i + 1]
+
+
+@pytest.mark.parametrize("name", ["relu", "gelu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+def test_activations_far_from_zero(name, t):
+    """Where a square of z is infinite in fp32 all of them are z or 0, and their
+    slopes 1 or 0, exactly."""
+    t = TYPES[t]
+    z = torch.tensor([[s * v for s in (1, -1) for v in (100.0, 1e10, 2e19, 1e25, 3e38)]]).to(t).repeat(5, 1)
+    dz, dm = (torch.empty_like(z, device="cuda") for _ in range(2))
+    one = torch.ones_like(z, device="cuda")
+    L.z1_linear_dz(one, dz, act=name, pre=z.cuda(), dmul=dm)
+    torch.cuda.synchronize()
+    assert torch.equal(dz.cpu(), (z > 0).to(t)) and torch.equal(dm.cpu(), z.clamp(min=0))

@@ -281,3 +281,26 @@ def test_weight_of_the_gradient_without_a_norm():
     assert B.lib.z1_qk_norm_rope_grad(ctypes.byref(a), 0x90000, 1 << 30, None) == B.Z1_EINVAL
     a = qk_args(q_weight=None, q_dweight=None, q_x=0x100001)
     assert B.lib.z1_qk_norm_rope_grad(ctypes.byref(a), 0x90000, 1 << 30, None) == B.Z1_EALIGN
+
+
+@pytest.mark.parametrize("over", [dict(y=0x10000), dict(y=0x20000), dict(y=0x30000), dict(y=0x60000), dict(pre=0x10000), dict(pre=0x20000),
+                                  dict(pre=0x30000), dict(pre=0x40000), dict(pre=0x50000)])
+def test_linear_refuses_outputs_over_other_buffers(over):
+    assert B.lib.z1_linear(ctypes.byref(linear_args(**over)), 0x90000, 1 << 30, None) == B.Z1_EINVAL
+
+
+@pytest.mark.parametrize("over", [dict(dx=0x10000), dict(dx=0x20000), dict(dx=0x30000), dict(dx=0x60000), dict(dweight=0x10000),
+                                  dict(dweight=0x20000), dict(dweight=0x30000), dict(dweight=0x40000)])
+def test_linear_grad_refuses_outputs_over_other_buffers(over):
+    assert B.lib.z1_linear_grad(ctypes.byref(grad_args(**over)), 0x90000, 1 << 30, None) == B.Z1_EINVAL
+
+
+@pytest.mark.parametrize("grad", [False, True])
+def test_qk_refuses_outputs_over_other_buffers(grad):
+    overs = [dict(q_out=0x100000, q_out_token=512), dict(q_out=0x100000, q_out_head=128), dict(q_out=0x210000), dict(q_out=0x200000)]
+    if grad:   # dout, of the same kind with other strides and of the other kind; one dweight for both
+        overs += [dict(q_out=0x120000, q_out_token=512), dict(q_out=0x220000), dict(q_dweight=0x240000)]
+    for over in overs:
+        a = qk_args(**over)
+        got = B.lib.z1_qk_norm_rope_grad(ctypes.byref(a), 0x90000, 1 << 30, None) if grad else B.lib.z1_qk_norm_rope(ctypes.byref(a), None)
+        assert got == B.Z1_EINVAL, over
