@@ -230,12 +230,39 @@ __device__ __forceinline__ void put_row(void *p, int64_t at, int n, const float 
         Eight<E>::store_some(to, v, n);
 }
 
+// A fetched row's words to a lane's own places in LDS, 64 lanes of 16 bytes apart, and
+// from there.
+template <typename RAW>
+__device__ __forceinline__ void park_words(char *to, const RAW &raw)
+{
+#pragma unroll
+    for (int w = 0; w < (int)(sizeof(RAW) / 16); ++w)
+        *reinterpret_cast<uint4v *>(to + w * 1024) = raw[w];
+}
+template <typename RAW>
+__device__ __forceinline__ void take_words(const char *from, RAW &raw)
+{
+#pragma unroll
+    for (int w = 0; w < (int)(sizeof(RAW) / 16); ++w)
+        raw[w] = *reinterpret_cast<const uint4v *>(from + w * 1024);
+}
+
 template <typename O>
 struct PlainOut {
     static constexpr bool kDrops = false;
     struct In {
         typename Eight<O>::Raw add;
     };
+    static __device__ __forceinline__ void park(const Epilogue &e, char *to, const In &in)
+    {
+        if (e.add)
+            park_words(to, in.add);
+    }
+    static __device__ __forceinline__ void take(const Epilogue &e, const char *from, In &in)
+    {
+        if (e.add)
+            take_words(from, in.add);
+    }
     static __device__ __forceinline__ void bias(const Epilogue &, int32_t, int, float (&)[8]) {}
     static __device__ __forceinline__ void fetch(const Epilogue &e, int64_t row, int32_t col, In &in)
     {
@@ -262,6 +289,20 @@ struct FullOut {
     struct In {
         typename Eight<E>::Raw mul, add;
     };
+    static __device__ __forceinline__ void park(const Epilogue &e, char *to, const In &in)
+    {
+        if (e.mul)
+            park_words(to, in.mul);
+        if (e.add)
+            park_words(to + sizeof(in.mul) * 64, in.add);
+    }
+    static __device__ __forceinline__ void take(const Epilogue &e, const char *from, In &in)
+    {
+        if (e.mul)
+            take_words(from, in.mul);
+        if (e.add)
+            take_words(from + sizeof(in.mul) * 64, in.add);
+    }
     static __device__ __forceinline__ void bias(const Epilogue &e, int32_t col, int n, float (&b)[8])
     {
         if (e.bias && n > 0)
@@ -441,58 +482,108 @@ __device__ __forceinline__ void put_parts(const Product &g, int32_t tp, int32_t 
                     float4v{acc[i][j][4 * r], acc[i][j][4 * r + 1], acc[i][j][4 * r + 2], acc[i][j][4 * r + 3]};
 }
 
-// A wave's sums into C, up to 64 rows of C at a time through its own part of the LDS, so that
-// TP * 4 lanes write TP * 32 elements of a row together.  Rows are 16 bytes longer than
-// their data, which spreads both accesses over the banks.  What the epilogue reads is
-// fetched kAhead rows early, into registers that it is used from: nothing else hides the
-// wait for it, and a copy of them would wait for the stores before it too.
-template <typename OUT, int TILE, int TP, int TQ>
-__device__ __forceinline__ void put_strips(const Product &g, int32_t tp, int32_t tq, int wp, int wq, int wave, int lane,
-                                           char *lds, const float16v (&acc)[TP][TQ])
+// A wave's sums into C, a strip of 32 or 64 rows of C at a time through its own part of
+// the LDS, so that TP * 4 lanes write TP * 32 elements of a row together.  Rows are 16
+// bytes longer than their data, which spreads both accesses over the banks.
+//
+// READS: the epilogue reads rows of its own (add, mul).  Those of a strip are fetched a
+// strip early, all at once, as nothing else hides the wait for them: 8192 x 2048 -> 8192
+// with a residual 332 us with two accesses of a lane under way, 265 so, 236 without a
+// residual.  They are parked in LDS too, so that the loop over the rows, with its
+// activations, need not be unrolled for the sake of the registers' names; strips are 32
+// rows then, as 64 with what is parked do not fit.  Without, 64 are faster (236 and 249).
+template <typename OUT, int TP, int TQ, bool READS>
+struct Strip {
+    static constexpr int kTall = READS || TQ < 2 ? 1 : 2;   // blocks of 32 rows
+    static constexpr int kRowBytes = TP * 128 + 16, kLanes = TP * 4, kRows = 64 / kLanes, kTurns = kTall * 32 / kRows;
+    static constexpr int kIn = (int)sizeof(typename OUT::In), kSums = kTall * 32 * kRowBytes;
+    static constexpr int kBytes = kSums + (READS ? kTurns * 64 * kIn : 0);   // of a wave
+};
+
+template <typename OUT, int TILE, bool READS, int TP, int TQ>
+__device__ __forceinline__ void put_strips_of(const Product &g, const Epilogue &e, int32_t tp, int32_t tq, int wp, int wq, int wave,
+                                              int lane, char *lds, const float16v (&acc)[TP][TQ])
 {
-    constexpr int kRowBytes = TP * 128 + 16, kLanes = TP * 4, kRows = 64 / kLanes;
-    constexpr int kTall = TQ < 2 ? TQ : 2, kAhead = kTall;   // small tiles have other workgroups beside them
-    const DropKey key = OUT::kDrops ? drop_key(g.e.drop) : DropKey{};
-    char *own = lds + wave * kTall * 32 * kRowBytes;
-    const int half = lane >> 5, low = lane & 31, at = lane % kLanes, row = lane / kLanes;
+    typedef Strip<OUT, TP, TQ, READS> S;
+    const DropKey key = OUT::kDrops ? drop_key(e.drop) : DropKey{};
+    char *own = lds + wave * S::kBytes, *parked = own + S::kSums + lane * 16;
+    const int half = lane >> 5, low = lane & 31, at = lane % S::kLanes, row = lane / S::kLanes;
     const int64_t p0 = (int64_t)tp * TILE + wp * TP * 32 + at * 8, q0 = (int64_t)tq * TILE + wq * TQ * 32 + row;
     const int n = (int)min((int64_t)8, g.P - p0);
     float b[8];
-    OUT::bias(g.e, (int32_t)p0, n, b);
-    typename OUT::In in[kAhead];
-    const auto fetch = [&](int r, typename OUT::In &to) {
-        if (n >= 8 && q0 + r < g.Q && r < TQ * 32)
-            OUT::fetch(g.e, q0 + r, (int32_t)p0, to);
+    OUT::bias(e, (int32_t)p0, n, b);
+    typename OUT::In in[S::kTurns];
+    const auto fetch = [&](int j) {
+#pragma unroll
+        for (int f = 0; f < S::kTurns; ++f)
+            if (n >= 8 && q0 + j * 32 + f * S::kRows < g.Q)
+                OUT::fetch(e, q0 + j * 32 + f * S::kRows, (int32_t)p0, in[f]);
     };
+    if (READS)
+        fetch(0);
 #pragma unroll
-    for (int f = 0; f < kAhead; ++f)
-        fetch(f * kRows, in[f]);
-#pragma unroll
-    for (int j = 0; j < TQ; j += kTall) {
+    for (int j = 0; j < TQ; j += S::kTall) {
         asm volatile("" ::: "memory");
 #pragma unroll
-        for (int k = 0; k < kTall; ++k)
+        for (int k = 0; k < S::kTall; ++k)
 #pragma unroll
             for (int i = 0; i < TP; ++i)
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    *reinterpret_cast<float4v *>(own + (k * 32 + low) * kRowBytes + (i * 32 + 8 * r + 4 * half) * 4) =
+                    *reinterpret_cast<float4v *>(own + (k * 32 + low) * S::kRowBytes + (i * 32 + 8 * r + 4 * half) * 4) =
                         float4v{acc[i][j + k][4 * r], acc[i][j + k][4 * r + 1], acc[i][j + k][4 * r + 2],
                                 acc[i][j + k][4 * r + 3]};
-        asm volatile("" ::: "memory");   // a wave's LDS accesses take place in order
-#pragma unroll 1
-        for (int r = 0; r < kTall * 32; r += kAhead * kRows)
+        if (READS) {
 #pragma unroll
-            for (int f = 0; f < kAhead; ++f) {
-                const int64_t q = q0 + j * 32 + r + f * kRows;
-                const char *from = own + (row + r + f * kRows) * kRowBytes + at * 32;
-                const float4v x = reinterpret_cast<const float4v *>(from)[0], y = reinterpret_cast<const float4v *>(from)[1];
-                float v[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+            for (int f = 0; f < S::kTurns; ++f)
+                OUT::park(e, parked + f * 64 * S::kIn, in[f]);
+            if (j + S::kTall < TQ)
+                fetch(j + S::kTall);
+        }
+        asm volatile("" ::: "memory");   // a wave's LDS accesses take place in order
+        // the next two turns' are read while two are worked on
+        float4v x[2][2];
+        typename OUT::In here[2];
+        const auto read = [&](int f, int u) {
+            const char *from = own + (row + f * S::kRows) * S::kRowBytes + at * 32;
+            x[u][0] = reinterpret_cast<const float4v *>(from)[0];
+            x[u][1] = reinterpret_cast<const float4v *>(from)[1];
+            if (READS)
+                OUT::take(e, parked + f * 64 * S::kIn, here[u]);
+        };
+        read(0, 0);
+        read(1, 1);
+#pragma unroll 1
+        for (int f = 0; f < S::kTurns; f += 2)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int64_t q = q0 + j * 32 + (f + u) * S::kRows;
+                float v[8] = {x[u][0][0], x[u][0][1], x[u][0][2], x[u][0][3], x[u][1][0], x[u][1][1], x[u][1][2], x[u][1][3]};
                 if (n > 0 && q < g.Q)
-                    OUT::put(g.e, key, q, (int32_t)p0, n, in[f], b, v);
-                fetch(j * 32 + r + (f + kAhead) * kRows, in[f]);
+                    OUT::put(e, key, q, (int32_t)p0, n, here[u], b, v);
+                if (f + 2 < S::kTurns)
+                    read(f + 2 + u, u);
             }
     }
+}
+
+template <typename OUT, int TILE, int TP, int TQ>
+__device__ __forceinline__ void put_strips(const Product &g, int32_t tp, int32_t tq, int wp, int wq, int wave, int lane,
+                                           char *lds, const float16v (&acc)[TP][TQ])
+{
+    if (g.e.add || g.e.mul)
+        return put_strips_of<OUT, TILE, true>(g, g.e, tp, tq, wp, wq, wave, lane, lds, acc);
+    Epilogue e = g.e;
+    e.add = e.mul = nullptr;
+    put_strips_of<OUT, TILE, false>(g, e, tp, tq, wp, wq, wave, lane, lds, acc);
+}
+
+// The LDS of a kernel's four waves: its ring, then the epilogue's strips.
+template <typename OUT, int TP, int TQ>
+constexpr int lds_of(int ring)
+{
+    const int a = 4 * Strip<OUT, TP, TQ, true>::kBytes, b = 4 * Strip<OUT, TP, TQ, false>::kBytes;
+    return ring > a ? (ring > b ? ring : b) : a > b ? a : b;
 }
 
 // A quarter of a panel of k_product_64 and k_product_128: multiplies a0 b0, reads the
@@ -607,7 +698,7 @@ __global__ __launch_bounds__(256) void k_product_64(Product g)
     constexpr int TILE = 64, RING = 3;
     typedef Side<E, PD, TILE, 4, 128> SP;
     typedef Side<E, QD, TILE, 4, 128> SQ;
-    __shared__ __align__(1024) char lds[RING * (SP::kBytes + SQ::kBytes)];
+    __shared__ __align__(1024) char lds[lds_of<OUT, 1, 1>(RING * (SP::kBytes + SQ::kBytes))];
     Setup<SP, SQ, TILE, 1, 1> u;
     u.start(g);
     float16v acc[1][1];
@@ -637,7 +728,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
     constexpr int TILE = 128, RING = 3;
     typedef Side<E, PD, TILE, 4, 128> SP;
     typedef Side<E, QD, TILE, 4, 128> SQ;
-    __shared__ __align__(1024) char lds[RING * (SP::kBytes + SQ::kBytes)];
+    __shared__ __align__(1024) char lds[lds_of<OUT, 2, 2>(RING * (SP::kBytes + SQ::kBytes))];
     Setup<SP, SQ, TILE, 2, 2> u;
     u.start(g);
     float16v acc[2][2];
@@ -756,6 +847,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
     typedef Side<E, PD, TILE, 4, 128> SP;
     typedef Side<E, QD, TILE, 4, 128> SQ;
     __shared__ __align__(1024) char lds[2 * SP::kBytes + 3 * SQ::kBytes];
+    static_assert(lds_of<OUT, 4, 4>(0) <= (int)sizeof(lds), "the epilogue's strips");
     Setup<SP, SQ, TILE, 4, 4> u;
     u.start(g);
     float16v acc[4][4];
