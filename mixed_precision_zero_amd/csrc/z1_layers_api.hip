@@ -10,6 +10,7 @@
 #include "z1_linear_tile.h"
 
 using namespace z1::host;
+using z1::ops::Copy;
 using z1::ops::Drop;
 using z1::ops::Epilogue;
 using z1::ops::Form;
@@ -99,8 +100,8 @@ Plan plan_product(Form form, int32_t dtype, const Matrix &p, const Matrix &q)
         }
         return Operand{m.p, ld * size, (int32_t)(deep ? m.rows : cols), (int32_t)(deep ? cols : m.rows)};
     };
+    g.q = operand(q, q_deep, w.pack_q, w.at_q);   // first: see run_product
     g.p = operand(p, p_deep, w.pack_p, w.at_p);
-    g.q = operand(q, q_deep, w.pack_q, w.at_q);
     g.P = (int32_t)(p_deep ? p.rows : p.cols);
     g.Q = (int32_t)(q_deep ? q.rows : q.cols);
     const int64_t bytes = std::max(g.p.depth, g.q.depth) * size;   // of depth
@@ -117,22 +118,26 @@ Plan plan_product(Form form, int32_t dtype, const Matrix &p, const Matrix &q)
     return w;
 }
 
+// has_q: Q's copy lies at the workspace's start from a product before this one, where any
+// product puts it, whichever way it reads Q.
 z1_status run_product(Form form, int32_t dtype, int32_t out_dtype, Plan &w, const Matrix &p, const Matrix &q,
-                      void *workspace, hipStream_t s)
+                      void *workspace, hipStream_t s, bool has_q = false)
 {
     Product &g = w.g;
     char *base = static_cast<char *>(workspace);
-    const auto pack = [&](const Matrix &m, int64_t at, Operand &o) {
-        o.base = base + at;
-        return z1::ops::launch_pack(dtype, m.p, m.ld, base + at, pad_to(m.cols, kPackCols), m.rows, m.cols, s);
-    };
-    hipError_t e = hipSuccess;
-    if (w.pack_p)
-        e = pack(p, w.at_p, g.p);
-    if (e == hipSuccess && w.pack_q)
-        e = pack(q, w.at_q, g.q);
     if (g.tile == 0)
         return status_of(z1::ops::launch_rows(dtype, g, s));
+    const auto copy = [&](bool pack, const Matrix &m, int64_t at, Operand &o) {
+        if (!pack)
+            return Copy{};
+        o.base = base + at;
+        return Copy{m.p, base + at, m.ld, m.rows, m.cols, pad_to(m.cols, kPackCols)};
+    };
+    Copy of_q = copy(w.pack_q, q, w.at_q, g.q);
+    const Copy of_p = copy(w.pack_p, p, w.at_p, g.p);
+    if (has_q)
+        of_q = Copy{};
+    hipError_t e = z1::ops::launch_pack(dtype, of_p, of_q, s);
     g.parts = reinterpret_cast<float *>(base + w.at_parts);
     if (e == hipSuccess)
         e = z1::ops::launch_product(form, dtype, out_dtype, g, s);
@@ -389,7 +394,8 @@ z1_status z1_linear_grad(const z1_linear_grad_args *a, void *workspace, int64_t 
     if (a->dweight && (a->rows > 0 || !a->accumulate)) {
         w.dw.g.e = Epilogue{a->dweight, nullptr, a->accumulate ? a->dweight : nullptr, nullptr, nullptr,
                             a->ld_dweight, 0, a->ld_dweight, 0, none, Z1_ACT_NONE};
-        return run_product(z1::ops::kWeight, a->dtype, a->dweight_dtype, w.dw, w.x, w.dz, workspace, hip(stream));
+        return run_product(z1::ops::kWeight, a->dtype, a->dweight_dtype, w.dw, w.x, w.dz, workspace, hip(stream),
+                           a->dx && a->rows > 0);
     }
     return Z1_OK;
 }

@@ -257,9 +257,15 @@ hipError_t launch_product(Form form, int32_t dtype, int32_t out_dtype, const Pro
 constexpr int64_t kRowsMost = 4;
 hipError_t launch_rows(int32_t dtype, const Product &g, hipStream_t s);
 
-// Copies rows of `cols` elements to rows of `cols_to`, zeros behind them.
-hipError_t launch_pack(int32_t dtype, const void *from, int64_t ld, void *to, int64_t cols_to, int64_t rows,
-                       int64_t cols, hipStream_t s);
+// Rows of `cols` elements to be copied to rows of `cols_to`, a multiple of eight, zeros
+// behind them.
+struct Copy {
+    const void *from;
+    void *to;
+    int64_t ld, rows, cols, cols_to;
+};
+// Both at once; rows 0: none.
+hipError_t launch_pack(int32_t dtype, const Copy &a, const Copy &b, hipStream_t s);
 
 // --------------------------------------------------------------------------
 // Elementwise layers

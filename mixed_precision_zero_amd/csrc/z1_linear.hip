@@ -1009,20 +1009,25 @@ hipError_t rows_of(const Product &g, hipStream_t s)
     return hipGetLastError();
 }
 
-// Eight elements of a row each; rows start anywhere and end in zeros.
+// Eight elements of a row each; rows start anywhere and end in zeros.  The first `first`
+// workgroups make copy a, the others b: one launch for both operands of a product (777 x
+// 333 in fp32 takes 3.5 us, most of it the launch).
 template <typename T>
-__global__ __launch_bounds__(256) void k_pack(const void *from, int64_t ld, void *to, int64_t cols_to, int64_t rows, int64_t cols)
+__global__ __launch_bounds__(256) void k_pack(Copy a, Copy b, uint32_t first)
 {
-    const int64_t per = cols_to / 8;
-    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < rows * per; i += gridDim.x * 256ll) {
-        const int64_t r = i / per, c = i % per * 8;
+    const bool second = blockIdx.x >= first;
+    const Copy c = second ? b : a;
+    const int64_t per = c.cols_to / 8, block = second ? blockIdx.x - first : blockIdx.x;
+    const int64_t blocks = second ? gridDim.x - first : first;
+    for (int64_t i = block * 256 + threadIdx.x; i < c.rows * per; i += blocks * 256) {
+        const int64_t r = i / per, at = i % per * 8;
         float v[8];
-        const typename T::store *p = static_cast<const typename T::store *>(from) + r * ld + c;
-        if (c + 8 <= cols)
+        const typename T::store *p = static_cast<const typename T::store *>(c.from) + r * c.ld + at;
+        if (at + 8 <= c.cols)
             Eight<T>::load(p, v);
         else
-            Eight<T>::load_some(p, v, (int)(cols - c));
-        Eight<T>::store(static_cast<typename T::store *>(to) + r * cols_to + c, v);
+            Eight<T>::load_some(p, v, (int)(c.cols - at));
+        Eight<T>::store(static_cast<typename T::store *>(c.to) + r * c.cols_to + at, v);
     }
 }
 
@@ -1048,17 +1053,16 @@ hipError_t launch_rows(int32_t dtype, const Product &g, hipStream_t s)
     }
 }
 
-hipError_t launch_pack(int32_t dtype, const void *from, int64_t ld, void *to, int64_t cols_to, int64_t rows,
-                       int64_t cols, hipStream_t s)
+hipError_t launch_pack(int32_t dtype, const Copy &a, const Copy &b, hipStream_t s)
 {
-    const int64_t n = rows * (cols_to / 8);
-    if (n == 0)
+    const auto grid = [](const Copy &c) { return (uint32_t)std::min<int64_t>((c.rows * (c.cols_to / 8) + 255) / 256, 8192); };
+    const uint32_t first = grid(a), all = first + grid(b);
+    if (all == 0)
         return hipSuccess;
-    const uint32_t grid = (uint32_t)std::min<int64_t>((n + 255) / 256, 8192);
     switch (dtype) {
-    case Z1_F32: k_pack<F32><<<grid, 256, 0, s>>>(from, ld, to, cols_to, rows, cols); break;
-    case Z1_BF16: k_pack<BF16><<<grid, 256, 0, s>>>(from, ld, to, cols_to, rows, cols); break;
-    default: k_pack<F16><<<grid, 256, 0, s>>>(from, ld, to, cols_to, rows, cols); break;
+    case Z1_F32: k_pack<F32><<<all, 256, 0, s>>>(a, b, first); break;
+    case Z1_BF16: k_pack<BF16><<<all, 256, 0, s>>>(a, b, first); break;
+    default: k_pack<F16><<<all, 256, 0, s>>>(a, b, first); break;
     }
     return hipGetLastError();
 }
