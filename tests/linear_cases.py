@@ -15,3 +15,7 @@ def forms(shape):
     """(P, Q, depth) of the three products of (rows, in, out)."""
     rows, inner, outer = shape
     return [(outer, rows, inner), (inner, rows, outer), (inner, outer, rows)]
+
+# x W' with odd rows and edges, by the tile side that it runs on
+EDGES = [(64, "f32", (130, 192, 75)), (64, "bf16", (130, 192, 75)), (128, "f16", (2041, 448, 2043)), (128, "f32", (8155, 484, 467)),
+         (256, "bf16", (4091, 320, 4093))]

@@ -5,8 +5,8 @@ adds one rounding a piece, which the depth's count already holds."""
 import pytest
 import torch
 
-from layer_refs import TYPES, U32, half_step, tiny
-from linear_cases import LARGE, PANELS, SPLIT
+from layer_refs import TYPES, U32, half_step, keep_mask, tiny
+from linear_cases import EDGES, LARGE, PANELS, SPLIT
 from mixed_precision_zero_amd import layers as L
 
 pytestmark = pytest.mark.gpu
@@ -84,3 +84,34 @@ def test_deep_products_in_pieces(case):
     again = torch.full((q, p), 2.0, device="cuda")
     L.z1_linear_grad(at, bt, None, dweight=again, accumulate=True, workspace=ws)
     assert torch.equal(dw, again)
+
+
+@pytest.mark.parametrize("side,kind,shape", EDGES)
+@pytest.mark.parametrize("what", ["", "residual", "bias", "pre drop", "mul", "mul residual bias drop", "relu", "relu mul residual"])
+def test_forms_of_the_epilogue(side, kind, shape, what):
+    """What an epilogue may have to do chooses its form; rows and edges of each on every
+    tile side.  y adds at most three roundings to z's, and the drop's scale one."""
+    rows, inner, outer = shape
+    t, what = TYPES[kind], what.split()
+    g = torch.Generator(device="cuda").manual_seed(rows + inner + outer)
+    rand = lambda *s: torch.randn(*s, generator=g, device="cuda").to(t)  # noqa: E731
+    x, w, b, m, r = rand(rows, inner), rand(outer, inner), rand(outer), rand(rows, outer), rand(rows, outer)
+    y, pre = torch.full_like(r, float("nan")), torch.full_like(r, float("nan"))
+    given = dict(bias=b, mul=m, residual=r, pre=pre, dropout=L.Dropout(torch.tensor([3, 5], device="cuda"), 0.25, 1))
+    L.z1_linear(x, w, y, act="relu" if "relu" in what else "none",
+                workspace=torch.empty(L.z1_linear_workspace(x, w), dtype=torch.uint8, device="cuda"),
+                **{k: v for k, v in given.items() if k in what or (k == "dropout" and "drop" in what)})
+    z, size = x.double() @ w.double().t(), x.double().abs() @ w.double().abs().t()
+    if "bias" in what:
+        z, size = z + b.double(), size + b.double().abs()
+    if "pre" in what:
+        near(pre, z, size, inner, t, "pre")
+    z = z.clamp(min=0) if "relu" in what else z
+    if "mul" in what:
+        z, size = z * m.double(), size * m.double().abs()
+    if "drop" in what:
+        kept = keep_mask(rows, outer, 3, 5 + 1, 0.25).cuda()
+        z, size = torch.where(kept, z / 0.75, torch.zeros_like(z)), size / 0.75
+    if "residual" in what:
+        z, size = z + r.double(), size + r.double().abs()
+    near(y, z, size, inner + 4, t, "y")

@@ -6,7 +6,7 @@ import subprocess
 
 import pytest
 
-from linear_cases import LARGE, PANELS, SPLIT, forms
+from linear_cases import EDGES, LARGE, PANELS, SPLIT, forms
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 PROGRAM = r"""
@@ -69,3 +69,9 @@ def test_pieces_cover_the_depth(choice):
         size = d * (4 if f else 2)
         assert tile in (64, 128, 256) and not (f and tile == 256)
         assert piece % 128 == 0 and splits * piece >= size and (splits - 1) * piece < size
+
+
+def test_the_edges_lie_on_every_tile_side(choice):
+    for side, kind, s in EDGES:
+        p, q, depth = forms(s)[0]
+        assert choice([(p, q, depth, kind == "f32")])[0][:2] == (side, 1), (side, kind, s)
