@@ -493,7 +493,7 @@ __device__ __forceinline__ void put_parts(const Product &g, int32_t tp, int32_t 
 // READS: the epilogue reads rows of its own (add, mul).  Those of a strip are fetched a
 // strip early, all at once, as nothing else hides the wait for them: 8192 x 2048 -> 8192
 // with a residual 332 us with two accesses of a lane under way, 265 so, 236 without a
-// residual.  They are parked in LDS too, so that the loop over the rows, with its
+// residual (now 250 and 221, in a form of their own).  They are parked in LDS too, so that the loop over the rows, with its
 // activations, need not be unrolled for the sake of the registers' names; strips are 32
 // rows then, as 64 with what is parked do not fit.  Without, 64 are faster (236 and 249).
 template <typename OUT, int TP, int TQ, bool READS>
