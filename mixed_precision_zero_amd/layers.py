@@ -133,9 +133,10 @@ class _Call:
         """Address of a contiguous tensor of at least `need` elements, or None."""
         if t is None:
             return None
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name}: expected a torch tensor, got {type(t).__name__}")
-        if t.dtype is not dtype or not t.is_contiguous() or t.numel() < need or t.get_device() != self.here:
+        if (getattr(t, "dtype", None) is not dtype or not t.is_contiguous() or t.numel() < need
+                or t.get_device() != self.here):
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"{name}: expected a torch tensor, got {type(t).__name__}")
             _checked([(t, name, dtype, need)])
             self.odd.append((t, name))
         return t.data_ptr()
@@ -331,16 +332,18 @@ def z1_linear_grad(dz, x, weight, *, dx=None, add=None, dweight=None, accumulate
 def _heads_of(call, t, name: str, dtype, shape):
     """(address, token stride, head stride) of [tokens, heads, dim] whose heads
     are contiguous and do not overlap; the addresses of no elements are null."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name}: expected a torch tensor, got {type(t).__name__}")
-    if t.dtype is not dtype:
+    if getattr(t, "dtype", None) is not dtype:
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name}: expected a torch tensor, got {type(t).__name__}")
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
     if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    n, h, d = shape
     if t.get_device() != call.here:
         call.odd.append((t, name))
+    n, h, d = shape
     st, sh, sd = t.stride()
+    if sd == 1 and n > 1 and sh >= d and st >= h * sh:
+        return t.data_ptr(), st, sh   # the usual order
     if sd != 1 and d > 1:
         raise ValueError(f"{name}: heads not contiguous")
     if h <= 1:
