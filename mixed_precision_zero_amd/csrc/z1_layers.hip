@@ -96,7 +96,7 @@ __global__ __launch_bounds__(256) void k_linear_dz(z1_linear_dz_args a, Drop d, 
     float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (n > 0) {
         for (int64_t r = r0 + rx; r < end; r += RX) {
-            float g[8], z[8], m[8];
+            float g[8], z[8] = {}, m[8];
             get8<T>(a.dy, r * a.ld_dy + c, n, g);
             if (a.pre)
                 get8<T>(a.pre, r * a.ld_pre + c, n, z);
@@ -104,26 +104,32 @@ __global__ __launch_bounds__(256) void k_linear_dz(z1_linear_dz_args a, Drop d, 
                 get8<T>(a.mul, r * a.ld_mul + c, n, m);
             if (key.on)
                 drop8(key, (uint32_t)(c >> 3), (uint32_t)r, g);
+            float value[8], slope[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                value[j] = z[j];
+                slope[j] = 1.f;
+            }
+            with_act(a.act, [&](auto k) {   // together: they share most of their work
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    value[j] = act_value<decltype(k)::value>(z[j]);
+                    slope[j] = act_slope<decltype(k)::value>(z[j]);
+                }
+            });
             if (a.dmul) {
-                float o[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    o[j] = z[j];
-                act_values(a.act, o);
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    o[j] *= g[j];
-                set8<T>(a.dmul, r * a.ld_dmul + c, n, o);
+                    value[j] *= g[j];
+                set8<T>(a.dmul, r * a.ld_dmul + c, n, value);
             }
             if (a.mul)
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
                     g[j] *= m[j];
-            with_act(a.act, [&](auto k) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    g[j] *= act_slope<decltype(k)::value>(z[j]);
-            });
+            for (int j = 0; j < 8; ++j)
+                g[j] *= slope[j];
             if (a.dz)
                 set8<T>(a.dz, r * a.ld_dz + c, n, g);
 #pragma unroll

@@ -395,3 +395,17 @@ def test_activations_far_from_zero(name, t):
     L.z1_linear_dz(one, dz, act=name, pre=z.cuda(), dmul=dm)
     torch.cuda.synchronize()
     assert torch.equal(dz.cpu(), (z > 0).to(t)) and torch.equal(dm.cpu(), z.clamp(min=0))
+
+
+def test_gelu_to_its_ends():
+    """Value and slope in fp32 relative to themselves.  Of Phi(-|z|), in U32: the fit 1, t 4
+    (argument and reciprocal) times at most 2.2, the polynomial 5, the exponential 3, three
+    products: at most 21, with its complement's no more; the value adds one, and the slope's
+    two terms may cancel."""
+    z = torch.cat([torch.linspace(-12.9, 12.9, 258001), torch.tensor([0.0, -0.0, 1e-30, -1e-30])]).float()[None]
+    dz, dm = (torch.empty_like(z, device="cuda") for _ in range(2))
+    L.z1_linear_dz(torch.ones_like(z, device="cuda"), dz, act="gelu", pre=z.cuda(), dmul=dm)
+    zd = z.double()
+    phi, bell = 0.5 * torch.erfc(-zd / 2 ** 0.5), torch.exp(-zd * zd / 2) / (2 * torch.pi) ** 0.5
+    near(dm, zd * phi, 22 * U32 * (zd * phi).abs() + 2.0 ** -126, "value")
+    near(dz, phi + zd * bell, 22 * U32 * (phi + (zd * bell).abs()) + 2.0 ** -126, "slope")
