@@ -129,7 +129,7 @@ z1_status z1_linear(const z1_linear_args *args, void *workspace, int64_t workspa
  *   dbias (+)= sum over rows of dz            fp32, from the unrounded dz
  * pre is needed for any act but NONE, and for dmul.  mul, dz, dmul and dbias
  * may be NULL (none; not all of the last three); the gradient of the residual
- * is dy itself.  dz may be dy or pre or mul, dmul may be mul or pre.
+ * is dy itself.  Where g is dropped dz and dmul are 0 whatever mul and pre are.  dz may be dy or pre or mul, dmul may be mul or pre.
  * accumulate 0 writes dbias, 1 adds to it.  act' is 0 at z = 0 for RELU.
  * ------------------------------------------------------------------------ */
 typedef struct z1_linear_dz_args {

@@ -96,14 +96,24 @@ __global__ __launch_bounds__(256) void k_linear_dz(z1_linear_dz_args a, Drop d, 
     float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (n > 0) {
         for (int64_t r = r0 + rx; r < end; r += RX) {
-            float g[8], z[8] = {}, m[8];
+            float g[8], z[8] = {}, m[8] = {};
             get8<T>(a.dy, r * a.ld_dy + c, n, g);
             if (a.pre)
                 get8<T>(a.pre, r * a.ld_pre + c, n, z);
             if (a.mul)
                 get8<T>(a.mul, r * a.ld_mul + c, n, m);
-            if (key.on)
-                drop8(key, (uint32_t)(c >> 3), (uint32_t)r, g);
+            if (key.on) {
+                // z and m too where dropped, as they may not be finite there
+                uint32_t w[4];
+                philox(key, (uint32_t)(c >> 3), (uint32_t)r, w);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const bool kept = drop_keeps(key, w, j);
+                    g[j] = kept ? g[j] * key.scale : 0.f;
+                    z[j] = kept ? z[j] : 0.f;
+                    m[j] = kept ? m[j] : 0.f;
+                }
+            }
             float value[8], slope[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {

@@ -61,16 +61,20 @@ __device__ __forceinline__ void philox(const DropKey &k, uint32_t block, uint32_
     w[3] = d;
 }
 
+// Whether the mask's words keep element j of eight.
+__device__ __forceinline__ bool drop_keeps(const DropKey &k, const uint32_t (&w)[4], int j)
+{
+    return (j & 1 ? w[j >> 1] >> 16 : w[j >> 1] & 0xffffu) >= k.threshold;
+}
+
 // Eight elements (row, 8 block ..) after dropout.
 __device__ __forceinline__ void drop8(const DropKey &k, uint32_t block, uint32_t row, float (&v)[8])
 {
     uint32_t w[4];
     philox(k, block, row, w);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const uint32_t u = j & 1 ? w[j >> 1] >> 16 : w[j >> 1] & 0xffffu;
-        v[j] = u >= k.threshold ? v[j] * k.scale : 0.f;
-    }
+    for (int j = 0; j < 8; ++j)
+        v[j] = drop_keeps(k, w, j) ? v[j] * k.scale : 0.f;
 }
 
 // Eight elements of type T at any alignment of T, in as few accesses as that
