@@ -130,7 +130,8 @@ z1_status z1_linear(const z1_linear_args *args, void *workspace, int64_t workspa
  * pre is needed for any act but NONE, and for dmul.  mul, dz, dmul and dbias
  * may be NULL (none; not all of the last three); the gradient of the residual
  * is dy itself.  Where g is dropped dz and dmul are 0 whatever mul and pre are.  dz may be dy or pre or mul, dmul may be mul or pre.
- * accumulate 0 writes dbias, 1 adds to it.  act' is 0 at z = 0 for RELU.
+ * accumulate 0 writes dbias, 1 adds to it.  act' is 0 at z = 0 for RELU; where pre
+ * is infinite (an fp16 one whose z was not) act and act' are their limits.
  * ------------------------------------------------------------------------ */
 typedef struct z1_linear_dz_args {
     int64_t rows, out;

@@ -123,7 +123,7 @@ __global__ __launch_bounds__(256) void k_linear_dz(z1_linear_dz_args a, Drop d, 
             with_act(a.act, [&](auto k) {   // together: they share most of their work
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    value[j] = act_value<decltype(k)::value>(z[j]);
+                    value[j] = act_value<decltype(k)::value>(z[j], above_low(z[j]));
                     slope[j] = act_slope<decltype(k)::value>(z[j]);
                 }
             });

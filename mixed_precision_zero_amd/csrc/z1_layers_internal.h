@@ -149,6 +149,13 @@ struct Eight {
 
 // act(z) and act'(z).  Written so that they hold at both ends: the sigmoid
 // underflows to 0 for z << 0, and Phi keeps its relative precision there.
+//
+// The gradient's pre may be infinite where z was not (one past fp16 is), so there both are
+// their limits: act takes `above_low(z)` for its factor z, which is finite where the other
+// factor is 0, and the slopes take their factor z between ends where theirs is.  NaN comes
+// through the other factors.  (8192 x 8192 fp16: SILU without a product 88 -> 91 us.)
+__device__ __forceinline__ float above_low(float z) { return __builtin_amdgcn_fmed3f(z, -1e30f, __builtin_inff()); }
+__device__ __forceinline__ float between_ends(float z) { return __builtin_amdgcn_fmed3f(z, -1e15f, 1e15f); }
 __device__ __forceinline__ float sigmoid(float z) { return __builtin_amdgcn_rcpf(1.f + expf(-z)); }
 __device__ __forceinline__ float gelu_tanh_arg(float z)
 {
@@ -159,15 +166,15 @@ __device__ __forceinline__ float gelu_tanh_arg(float z)
 //   Phi(-|z|) = erfc(u) / 2 = exp(-z^2 / 2) t Q(t) / 2,   t = 1 / (1 + 0.3 u)
 // with a Q of degree 8 fitted to exp(u^2) erfc(u) / t over u in [0, 11] by least squares,
 // reweighted until its relative error was even: 2e-8.  z^2 is taken with its rounding, as
-// the exponential multiplies that by z^2 / 2.  Behind |z| = 16 both are 0 in fp32.  8192 x
-// 2048 -> 8192 with bias and GELU: 314 us, 344 with the library's erfc; its gradient of 8192 x 8192,
-// with a product: 143 and 230.
+// the exponential multiplies that by z^2 / 2.  Behind |z| = 16 both are 0 in fp32; NaN
+// is not behind it.  8192 x 2048 -> 8192 with bias and GELU: 314 us, 344 with the library's
+// erfc; its gradient of 8192 x 8192, with a product: 143 and 230.
 struct Normal {
     float bell, below;
 };
 __device__ __forceinline__ Normal normal_of(float z)
 {
-    const float s = fminf(fabsf(z), 16.f), square = s * s;
+    const float s = fabsf(z) > 16.f ? 16.f : fabsf(z), square = s * s;
     const float e = expf(-0.5f * square), bell = fmaf(-0.5f * e, fmaf(s, s, -square), e);
     const float t = __builtin_amdgcn_rcpf(fmaf(s, 0.212132034f, 1.f));
     float q = -0.129556016f;
@@ -183,17 +190,18 @@ __device__ __forceinline__ Normal normal_of(float z)
     return Normal{bell, z < 0.f ? tail : 1.f - tail};
 }
 
+// factor: z, or above_low(z)
 template <int ACT>
-__device__ __forceinline__ float act_value(float z)
+__device__ __forceinline__ float act_value(float z, float factor)
 {
     if constexpr (ACT == Z1_ACT_RELU)
         return z < 0.f ? 0.f : z;
     if constexpr (ACT == Z1_ACT_GELU)
-        return z * normal_of(z).below;
+        return factor * normal_of(z).below;
     if constexpr (ACT == Z1_ACT_GELU_TANH)
-        return z * sigmoid(gelu_tanh_arg(z));
+        return factor * sigmoid(gelu_tanh_arg(z));
     if constexpr (ACT == Z1_ACT_SILU)
-        return z * sigmoid(z);
+        return factor * sigmoid(z);
     if constexpr (ACT == Z1_ACT_RELU2) {
         const float r = z < 0.f ? 0.f : z;
         return r * r;
@@ -208,16 +216,15 @@ __device__ __forceinline__ float act_slope(float z)
         return z > 0.f ? 1.f : 0.f;
     if constexpr (ACT == Z1_ACT_GELU) {
         const Normal n = normal_of(z);
-        return fmaf(z * 0.39894228040143268f, n.bell, n.below);
+        return fmaf(between_ends(z) * 0.39894228040143268f, n.bell, n.below);
     }
     if constexpr (ACT == Z1_ACT_GELU_TANH) {
-        const float s = sigmoid(gelu_tanh_arg(z));
-        // s (1 - s) is 0 long before z^2 is infinite
-        return fmaf(z * s * (1.f - s), 1.5957691216057308f * fmaf(3.f * 0.044715f, fminf(z * z, 1e30f), 1.f), s);
+        const float s = sigmoid(gelu_tanh_arg(z)), f = between_ends(z);
+        return fmaf(f * s * (1.f - s), 1.5957691216057308f * fmaf(3.f * 0.044715f, f * f, 1.f), s);
     }
     if constexpr (ACT == Z1_ACT_SILU) {
         const float s = sigmoid(z);
-        return s * fmaf(z, 1.f - s, 1.f);
+        return s * fmaf(between_ends(z), 1.f - s, 1.f);
     }
     if constexpr (ACT == Z1_ACT_RELU2)
         return 2.f * (z < 0.f ? 0.f : z);
@@ -243,7 +250,7 @@ __device__ __forceinline__ void act_values(int32_t act, float (&v)[8])
     with_act(act, [&](auto a) {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            v[j] = act_value<decltype(a)::value>(v[j]);
+            v[j] = act_value<decltype(a)::value>(v[j], v[j]);
     });
 }
 
