@@ -94,7 +94,8 @@ z1_status z1_dropout(const z1_dropout_args *args, z1_stream stream);
  *            GELU_TANH z / (1 + exp(-2 sqrt(2 / pi) (z + 0.044715 z^3))),
  *            RELU2 max(z, 0)^2
  * rows in [0, 2^30], in and out in [1, 2^20], row distances of x and weight
- * below 2^21.
+ * below 2^21; an output of any of the products has fewer than 2^24 tiles of 256 x
+ * 256 elements (fp32: 128 x 128), which one that fits the GPU has by far.
  * ------------------------------------------------------------------------ */
 typedef enum z1_act {
     Z1_ACT_NONE = 0, Z1_ACT_RELU = 1, Z1_ACT_GELU = 2, Z1_ACT_GELU_TANH = 3, Z1_ACT_SILU = 4,

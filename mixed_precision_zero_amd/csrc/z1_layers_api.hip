@@ -72,6 +72,7 @@ bool in_place(const Matrix &m, int32_t dtype)
 struct Plan {
     Product g{};
     bool pack_p = false, pack_q = false;
+    bool fits = true;   // a launch
     int64_t at_p = 0, at_q = 0, at_parts = 0, bytes = 0;
 };
 
@@ -106,6 +107,10 @@ Plan plan_product(Form form, int32_t dtype, const Matrix &p, const Matrix &q)
     g.Q = (int32_t)(q_deep ? q.rows : q.cols);
     const int64_t bytes = std::max(g.p.depth, g.q.depth) * size;   // of depth
     const z1::ops::TileChoice c = z1::ops::pick_product(g.P, g.Q, bytes, dtype == Z1_F32);
+    if (c.tile == 0) {
+        w.fits = false;
+        return w;
+    }
     g.tile = c.tile;
     g.splits = c.splits;
     g.piece = c.piece;
@@ -164,7 +169,7 @@ z1_status linear_plan(const z1_linear_args *a, Matrix &x, Matrix &weight, Plan &
     if (!operand_ok(x) || !operand_ok(weight))
         return Z1_EINVAL;
     w = plan_product(z1::ops::kForward, a->dtype, weight, x);
-    return Z1_OK;
+    return w.fits ? Z1_OK : Z1_EINVAL;
 }
 
 struct GradPlan {
@@ -192,7 +197,7 @@ z1_status linear_grad_plan(const z1_linear_grad_args *a, GradPlan &w)
         w.dw = plan_product(z1::ops::kWeight, a->dtype, w.x, w.dz);
         w.bytes = std::max(w.bytes, w.dw.bytes);
     }
-    return Z1_OK;
+    return w.dx.fits && w.dw.fits ? Z1_OK : Z1_EINVAL;
 }
 
 z1_status workspace_ok(const void *workspace, int64_t have, int64_t need)

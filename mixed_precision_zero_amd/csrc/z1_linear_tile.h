@@ -12,10 +12,12 @@ namespace z1 {
 namespace ops {
 
 struct TileChoice {
-    int32_t tile;     // 64, 128 or 256
+    int32_t tile;     // 64, 128 or 256; 0: none that can be launched
     int32_t splits;   // pieces of the depth
     int32_t piece;    // bytes of depth each of them takes, a multiple of 128
 };
+
+constexpr int64_t kMostGroups = (INT64_C(1) << 24) - 1;   // of a launch: 2^32 - 1 threads, 256 each
 
 // The choice with the smallest estimate of its time in microseconds, for a product of
 // P x Q elements and `bytes` of depth, fp32 or 16-bit.  With t workgroups to each of 256
@@ -29,9 +31,12 @@ struct TileChoice {
 // bf16 forward): 2048^3 29 / 22 / 52, 1024 x 4096 -> 4096 55 / 37 / 83, 2048 x 576 -> 1536
 // 9.2 / 11.3 / 29, 1000^3 7.5 / 12.6 / 35, 4096^3 197 / 150 / 117; fp32 1000^3 23 / 67,
 // 2048^3 140 / 140.
+//
+// Only what a launch can hold is chosen from (a shallow product of 2^29 rows has 2^24
+// tiles of 64 for 128 outputs), with pieces of less than 2^31 bytes.
 inline TileChoice pick_product(int64_t P, int64_t Q, int64_t bytes, bool fp32)
 {
-    TileChoice best{64, 1, 128};
+    TileChoice best{0, 0, 0};
     double least = 0.0;
     const int64_t panels = std::max<int64_t>(1, (bytes + 127) / 128);
     for (const int side : {64, 128, 256}) {
@@ -39,9 +44,12 @@ inline TileChoice pick_product(int64_t P, int64_t Q, int64_t bytes, bool fp32)
             continue;
         const int64_t tiles = ((P + side - 1) / side) * ((Q + side - 1) / side);
         for (int64_t s = 1; s <= 64 && s <= panels; s = s < 4 ? s + 1 : s + s / 2) {
-            if (s > 1 && (panels / s < 4 || tiles * s > 1024))
+            if (tiles * s > kMostGroups || (s > 1 && (panels / s < 4 || tiles * s > 1024)))
                 break;
-            const double n = (double)((panels + s - 1) / s), t = (double)(tiles * s) / 256.0, r = ceil(t);
+            const int64_t piece = (panels + s - 1) / s;
+            if (piece * 128 > INT32_MAX)
+                continue;
+            const double n = (double)piece, t = (double)(tiles * s) / 256.0, r = ceil(t);
             double cost;
             if (side == 64)
                 cost = 3.9 + 0.55 * t + n * (fp32 ? std::max(0.54, 0.5 * t) : std::max(0.14 + 0.08 * t, 0.175 * t));
@@ -53,7 +61,6 @@ inline TileChoice pick_product(int64_t P, int64_t Q, int64_t bytes, bool fp32)
                 cost += 4.0 + 8e-6 * (double)s * (double)P * (double)Q / 4.0;
             if (least == 0.0 || cost < least) {
                 least = cost;
-                const int64_t piece = (panels + s - 1) / s;
                 best = TileChoice{side, (int32_t)((panels + piece - 1) / piece), (int32_t)(piece * 128)};
             }
         }
