@@ -47,6 +47,11 @@ bool among(const void *p, std::initializer_list<const void *> others)
     return p && std::find(others.begin(), others.end(), p) != others.end();
 }
 
+const void *read_rng(const z1_drop &d) { return d.p > 0.0 ? d.rng : nullptr; }
+
+// A workspace of which no byte is needed is no buffer of the call.
+const void *used(const void *workspace, int64_t need) { return need > 0 ? workspace : nullptr; }
+
 // --------------------------------------------------------------------------
 // Products
 // --------------------------------------------------------------------------
@@ -223,7 +228,23 @@ bool heads_ok(const z1_heads &k, int64_t tokens, bool grad)
            (!grad || apart(k.dout, k.dout_token, k.dout_head));
 }
 
-z1_status qk_check(const z1_qk_args *a, bool grad)
+// Whether an output of the call is another buffer of it that it may not be.  work: the
+// workspace, where one is used.
+bool qk_overlap(const z1_qk_args *a, bool grad, const void *work)
+{
+    const z1_heads &q = a->q, &k = a->k;
+    const bool has_q = a->tokens > 0 && q.heads > 0, has_k = a->tokens > 0 && k.heads > 0;
+    const auto of = [](bool there, const void *p) { return there ? p : nullptr; };
+    const void *q_out = of(has_q, q.out), *k_out = of(has_k, k.out), *q_dw = of(grad, q.dweight), *k_dw = of(grad, k.dweight);
+    const void *q_x = of(has_q, q.x), *k_x = of(has_k, k.x), *q_w = of(has_q, q.weight), *k_w = of(has_k, k.weight);
+    const void *q_dout = of(has_q && grad, q.dout), *k_dout = of(has_k && grad, k.dout);
+    const void *at = of(has_q || has_k, a->positions), *freq = of(has_q || has_k, a->inv_freq);
+    return among(q_out, {k_out, k_x, k_dout, q_w, k_w, q_dw, k_dw, at, freq}) || among(k_out, {q_x, q_dout, q_w, k_w, q_dw, k_dw, at, freq}) ||
+           among(q_dw, {k_dw, q_x, k_x, q_dout, k_dout, q_w, k_w, at, freq}) || among(k_dw, {q_x, k_x, q_dout, k_dout, q_w, k_w, at, freq}) ||
+           among(work, {q_out, k_out, q_dw, k_dw, q_x, k_x, q_dout, k_dout, q_w, k_w, at, freq});
+}
+
+z1_status qk_check(const z1_qk_args *a, bool grad, const void *work = nullptr)
 {
     if (!a || a->tokens < 0 || a->tokens > INT32_MAX || a->dim < 1 || a->dim > 512 || a->n_freq < 0 ||
         a->n_freq > a->dim / 2 || !dtype_ok(a->dtype) || !itype_ok(a->position_type) || !(a->eps >= 0.0) ||
@@ -232,10 +253,9 @@ z1_status qk_check(const z1_qk_args *a, bool grad)
         return Z1_EINVAL;
     if ((a->tokens > 0 && !a->positions) || (a->n_freq > 0 && !a->inv_freq))
         return Z1_EINVAL;
-    if (grad && ((a->q.dweight && !a->q.weight) || (a->k.dweight && !a->k.weight) || among(a->q.dweight, {a->k.dweight})))
+    if (grad && ((a->q.dweight && !a->q.weight) || (a->k.dweight && !a->k.weight)))
         return Z1_EINVAL;
-    if (a->tokens > 0 && a->q.heads > 0 && a->k.heads > 0 &&
-        (among(a->q.out, {a->k.out, a->k.x, grad ? a->k.dout : nullptr}) || among(a->k.out, {a->q.x, grad ? a->q.dout : nullptr})))
+    if (qk_overlap(a, grad, work))
         return Z1_EINVAL;
     const size_t size = type_size(a->dtype);
     for (const z1_heads *k : {&a->q, &a->k})
@@ -258,6 +278,8 @@ z1_status z1_dropout(const z1_dropout_args *a, z1_stream stream)
         !rows_ok(a->y, a->rows, a->cols, a->ld_y, true) || !rows_ok(a->residual, a->rows, a->cols, a->ld_residual, false))
         return Z1_EINVAL;
     if (a->rows > 1 && ((a->y == a->x && a->ld_y != a->ld_x) || (a->y == a->residual && a->ld_y != a->ld_residual)))
+        return Z1_EINVAL;
+    if (a->rows > 0 && among(a->y, {read_rng(a->drop)}))
         return Z1_EINVAL;
     const size_t size = type_size(a->dtype);
     if (!aligned(a->x, size) || !aligned(a->y, size) || !aligned(a->residual, size) || !aligned(a->drop.rng, 8))
@@ -287,8 +309,10 @@ z1_status z1_linear(const z1_linear_args *a, void *workspace, int64_t workspace_
         return Z1_EINVAL;
     if (a->rows > 1 && ((a->y == a->residual && a->ld_y != a->ld_residual) || (a->y == a->mul && a->ld_y != a->ld_mul)))
         return Z1_EINVAL;
-    if (a->rows > 0 && (among(a->y, {a->x, a->weight, a->bias, a->pre}) ||
-                        among(a->pre, {a->x, a->weight, a->bias, a->mul, a->residual})))
+    const void *rng = read_rng(a->drop);
+    if (a->rows > 0 &&
+        (among(a->y, {a->x, a->weight, a->bias, a->pre, rng}) || among(a->pre, {a->x, a->weight, a->bias, a->mul, a->residual, rng}) ||
+         among(used(workspace, w.bytes), {a->x, a->weight, a->bias, a->mul, a->residual, a->pre, a->y, rng})))
         return Z1_EINVAL;
     const z1_status ws = workspace_ok(workspace, workspace_bytes, w.bytes);
     if (ws == Z1_EINVAL)
@@ -335,7 +359,10 @@ z1_status z1_linear_dz(const z1_linear_dz_args *a, void *workspace, int64_t work
         ((a->dz == a->dy && a->ld_dz != a->ld_dy) || (a->dz == a->pre && a->ld_dz != a->ld_pre) ||
          (a->dz == a->mul && a->ld_dz != a->ld_mul)))
         return Z1_EINVAL;
-    if (a->dmul && (a->dmul == a->dz || a->dmul == a->dy))
+    const void *rng = read_rng(a->drop);
+    if (a->rows > 0 &&
+        (among(a->dmul, {a->dz, a->dy, rng}) || among(a->dz, {rng}) || among(a->dbias, {a->dy, a->pre, a->mul, a->dz, a->dmul, rng}) ||
+         among(used(workspace, need), {a->dy, a->pre, a->mul, a->dz, a->dmul, a->dbias, rng})))
         return Z1_EINVAL;
     if (a->rows > 1 && a->dmul &&
         ((a->dmul == a->pre && a->ld_dmul != a->ld_pre) || (a->dmul == a->mul && a->ld_dmul != a->ld_mul)))
@@ -375,7 +402,9 @@ z1_status z1_linear_grad(const z1_linear_grad_args *a, void *workspace, int64_t 
         return Z1_EINVAL;
     // dx is written before dweight is computed; without dweight x is not read
     if (a->rows > 0 && (among(a->dx, {a->dz, a->weight, a->dweight, a->dweight ? a->x : nullptr}) ||
-                        among(a->dweight, {a->dz, a->x, a->dx ? a->weight : nullptr, a->dx ? a->add : nullptr})))
+                        among(a->dweight, {a->dz, a->x, a->dx ? a->weight : nullptr, a->dx ? a->add : nullptr}) ||
+                        among(used(workspace, w.bytes), {a->dz, a->dweight ? a->x : nullptr, a->dx ? a->weight : nullptr,
+                                                         a->dx ? a->add : nullptr, a->dx, a->dweight})))
         return Z1_EINVAL;
     const z1_status ws = workspace_ok(workspace, workspace_bytes, w.bytes);
     if (ws == Z1_EINVAL)
@@ -426,13 +455,13 @@ z1_status z1_qk_norm_rope_grad_workspace(int64_t tokens, int64_t q_heads, int64_
 
 z1_status z1_qk_norm_rope_grad(const z1_qk_args *a, void *workspace, int64_t workspace_bytes, z1_stream stream)
 {
-    const z1_status st = qk_check(a, true);
+    int64_t need = 0;
+    const bool sums = a && (a->q.dweight || a->k.dweight);
+    if (sums && z1_qk_norm_rope_grad_workspace(a->tokens, a->q.heads, a->k.heads, a->dim, &need) != Z1_OK)
+        return Z1_EINVAL;
+    const z1_status st = qk_check(a, true, used(workspace, need));
     if (st == Z1_EINVAL)
         return st;
-    int64_t need = 0;
-    const bool sums = a->q.dweight || a->k.dweight;
-    if (sums)
-        (void)z1_qk_norm_rope_grad_workspace(a->tokens, a->q.heads, a->k.heads, a->dim, &need);
     const z1_status ws = workspace_ok(workspace, workspace_bytes, need);
     if (ws == Z1_EINVAL)
         return ws;
