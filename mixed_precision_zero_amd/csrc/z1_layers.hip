@@ -339,16 +339,18 @@ __device__ __forceinline__ int64_t position_of(const z1_qk_args &a, int64_t t)
                                      : static_cast<const int64_t *>(a.positions)[t];
 }
 
-// The token's (cos, sin) of every frequency into the wave's LDS.  The angle is reduced to
-// a part of a turn in binary64.
+// The token's (cos, sin) of every frequency into the wave's LDS.  The angle in binary64 is
+// reduced to a part of a turn with 1 / (2 pi) in two parts and the product's own rounding,
+// so that the part is exact to fp32 up to angles of 2^53.
 __device__ __forceinline__ void put_turns(const z1_qk_args &a, int64_t t, float2 *lds, int lane)
 {
     const double pos = (double)position_of(a, t);
     asm volatile("" ::: "memory");
     for (int f = lane; f < a.n_freq; f += 64) {
-        const double turn = pos * a.inv_freq[f] * 0.15915494309189533577;
+        const double angle = pos * a.inv_freq[f], turn = angle * 0.15915494309189535;
+        const double rest = fma(angle, -9.839338337591243e-18, fma(angle, 0.15915494309189535, -turn));
         float s, c;
-        sincospif((float)(turn - rint(turn)) * 2.f, &s, &c);
+        sincospif((float)((turn - rint(turn)) + rest) * 2.f, &s, &c);
         lds[f] = make_float2(c, s);
     }
     // one wave's LDS accesses take place in order
