@@ -162,7 +162,8 @@ __device__ __forceinline__ float gelu_tanh_arg(float z)
     return 1.5957691216057308f * z * fmaf(0.044715f * z, z, 1.f);   // 2 sqrt(2 / pi)
 }
 
-// exp(-z^2 / 2) and Phi(z), both to 1e-6 of themselves.  For u = |z| / sqrt(2),
+// exp(-z^2 / 2) and Phi(z), both to 1e-6 of themselves while they are normal numbers (|z| <
+// 12.9).  For u = |z| / sqrt(2),
 //   Phi(-|z|) = erfc(u) / 2 = exp(-z^2 / 2) t Q(t) / 2,   t = 1 / (1 + 0.3 u)
 // with a Q of degree 8 fitted to exp(u^2) erfc(u) / t over u in [0, 11] by least squares,
 // reweighted until its relative error was even: 2e-8.  z^2 is taken with its rounding, as
